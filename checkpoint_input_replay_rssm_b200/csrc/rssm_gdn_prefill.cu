@@ -1,0 +1,214 @@
+// rssm_gdn_prefill.cu -- the gated delta rule over packed prompts (rssm_gdn_prefill):
+// every token's output and the fp32 state after each prompt, which a replay decode
+// starts from (rssm_import_state).
+//
+// Recurrent form, for any supported shape and input type, all arithmetic fp32.  The
+// state's rows are independent (row p meets only v[p]), so a warp owns 8 of them and
+// keeps them in registers over the whole prompt.  Per token and row s:
+//   a = alpha s,  c = beta (v[p] - a . k),  o[p] = a . q + c (k . q),  s = a + c k
+// The output is written from the decayed old state, so that the three dot products
+// a.k, a.q, k.q are one reduction (8 lanes, 3 shuffles) instead of two in sequence:
+// the chain through the reduction bounds this kernel, not HBM.  A row's columns lie
+// over 8 lanes in float4 pieces, 4 lane groups of 2 rows each.  Tokens are staged 16 at
+// a time in shared memory (fp32), the next 16 in flight meanwhile.
+#include "rssm_internal.h"
+#include "rssm_packed.cuh"
+
+namespace rssm {
+
+namespace {
+
+struct GdnPreArgs {
+    int B, H, P, tokens;
+    const void *q, *k, *v;      // [tokens][H][N], [tokens][H][N], [tokens][H][P]
+    const float *alpha, *beta;  // [tokens][H]
+    const int32_t *cu;          // [B + 1]
+    const float *S0;            // [B][H][P][N] or nullptr
+    float *y, *S_out;
+    int32_t *err;
+};
+
+constexpr int kRecWarps = 4;             // 8 state rows each
+constexpr int kRecRows = 8 * kRecWarps;  // rows of one CTA
+constexpr int kRecTok = 16;              // tokens staged at a time
+
+template <typename IN> __device__ __forceinline__ float in_value(const void *p, int64_t i);
+template <> __device__ __forceinline__ float in_value<float>(const void *p, int64_t i) { return ((const float *)p)[i]; }
+template <> __device__ __forceinline__ float in_value<__nv_bfloat16>(const void *p, int64_t i) {
+    return __bfloat162float(((const __nv_bfloat16 *)p)[i]);
+}
+
+template <typename IN, int N>
+__global__ void __launch_bounds__(32 * kRecWarps) gdn_recurrent_kernel(const GdnPreArgs a) {
+    constexpr int kThr = 32 * kRecWarps;
+    constexpr int V = N >= 32 ? 4 : 2;  // columns per piece
+    constexpr int J = N / (8 * V);      // pieces per lane
+    constexpr int NQ = kRecTok * N / kThr, NV = kRecTok * kRecRows / kThr;
+    __shared__ __align__(16) float sk[2][kRecTok][N], sq[2][kRecTok][N];
+    __shared__ float sv[2][kRecTok][kRecRows], sa[2][kRecTok], sb[2][kRecTok];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int l8 = lane & 7, g4 = lane >> 3;
+    const int h = blockIdx.y, b = blockIdx.z, p0 = blockIdx.x * kRecRows;
+    const int rows = min(kRecRows, a.P - p0);
+    int r0, r1;
+    if (!packed_rows(a.cu, b, a.tokens, r0, r1)) {
+        if (tid == 0) report_opt(a.err, DEV_BAD_LENGTHS, b, h, r1);
+        return;
+    }
+    const int64_t head = (int64_t)b * a.H + h;
+    const int row0 = 8 * warp + 2 * g4;  // this lane group's rows: row0, row0 + 1 (P is a multiple of 8)
+    const bool on = row0 < rows;
+    float s[2][J][V];
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                s[r][j][e] = on && a.S0 ? a.S0[(head * a.P + p0 + row0 + r) * N + j * 8 * V + l8 * V + e] : 0.f;
+
+    float rk[NQ], rq[NQ], rv[NV], ra = 0.f, rb = 0.f;
+    auto fetch = [&](int t0) {
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) {
+            const int e = tid + i * kThr, t = e / N, n = e % N;
+            const int64_t at = ((int64_t)(t0 + t) * a.H + h) * N + n;
+            const bool live = t0 + t < r1;
+            rk[i] = live ? in_value<IN>(a.k, at) : 0.f;
+            rq[i] = live ? in_value<IN>(a.q, at) : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int e = tid + i * kThr, t = e / kRecRows, p = e % kRecRows;
+            rv[i] = t0 + t < r1 && p < rows ? in_value<IN>(a.v, ((int64_t)(t0 + t) * a.H + h) * a.P + p0 + p) : 0.f;
+        }
+        if (tid < kRecTok) {
+            const bool live = t0 + tid < r1;
+            ra = live ? a.alpha[(int64_t)(t0 + tid) * a.H + h] : 0.f;
+            rb = live ? a.beta[(int64_t)(t0 + tid) * a.H + h] : 0.f;
+        }
+    };
+    auto put = [&](int buf) {
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) {
+            const int e = tid + i * kThr;
+            sk[buf][e / N][e % N] = rk[i];
+            sq[buf][e / N][e % N] = rq[i];
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int e = tid + i * kThr;
+            sv[buf][e / kRecRows][e % kRecRows] = rv[i];
+        }
+        if (tid < kRecTok) {
+            sa[buf][tid] = ra;
+            sb[buf][tid] = rb;
+        }
+    };
+
+    int buf = 0;
+    if (r0 < r1) fetch(r0);
+    for (int t0 = r0; t0 < r1; t0 += kRecTok, buf ^= 1) {
+        put(buf);  // the other buffer's readers passed the barrier of the step before
+        __syncthreads();
+        if (t0 + kRecTok < r1) fetch(t0 + kRecTok);
+        const int nt = min(kRecTok, r1 - t0);
+        for (int t = 0; t < nt; ++t) {
+            const float al = sa[buf][t];
+            float dk[2] = {0.f, 0.f}, dq[2] = {0.f, 0.f}, kq = 0.f, kv[J][V];
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    const float kk = sk[buf][t][j * 8 * V + l8 * V + e], qq = sq[buf][t][j * 8 * V + l8 * V + e];
+                    kv[j][e] = kk;
+                    kq = fmaf(kk, qq, kq);
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        s[r][j][e] *= al;
+                        dk[r] = fmaf(s[r][j][e], kk, dk[r]);
+                        dq[r] = fmaf(s[r][j][e], qq, dq[r]);
+                    }
+                }
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) {
+                kq += __shfl_xor_sync(0xffffffffu, kq, o);
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    dk[r] += __shfl_xor_sync(0xffffffffu, dk[r], o);
+                    dq[r] += __shfl_xor_sync(0xffffffffu, dq[r], o);
+                }
+            }
+            const float be = sb[buf][t];
+            float o[2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const float c = be * (sv[buf][t][row0 + r] - dk[r]);
+                o[r] = fmaf(c, kq, dq[r]);
+#pragma unroll
+                for (int j = 0; j < J; ++j)
+#pragma unroll
+                    for (int e = 0; e < V; ++e) s[r][j][e] = fmaf(c, kv[j][e], s[r][j][e]);
+            }
+            if (l8 == 0 && on)
+                *reinterpret_cast<float2 *>(a.y + ((int64_t)(t0 + t) * a.H + h) * a.P + p0 + row0) =
+                    make_float2(o[0], o[1]);
+        }
+    }
+    if (on)
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+                    a.S_out[(head * a.P + p0 + row0 + r) * N + j * 8 * V + l8 * V + e] = s[r][j][e];
+}
+
+template <typename IN>
+cudaError_t launch_recurrent(const GdnPreArgs &a, int N, cudaStream_t st) {
+    auto k = N == 16 ? gdn_recurrent_kernel<IN, 16>
+                     : N == 32 ? gdn_recurrent_kernel<IN, 32>
+                               : N == 64 ? gdn_recurrent_kernel<IN, 64> : gdn_recurrent_kernel<IN, 128>;
+    k<<<dim3((a.P + kRecRows - 1) / kRecRows, a.H, a.B), 32 * kRecWarps, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+bool gdn_prefill_valid(const rssm_gdn_prefill_config *c) {
+    return c && c->batch >= 1 && c->batch <= 65535 && c->nheads >= 1 && c->nheads <= 65535 && c->headdim >= 8 &&
+           c->headdim <= 256 && c->headdim % 8 == 0 &&
+           (c->dstate == 16 || c->dstate == 32 || c->dstate == 64 || c->dstate == 128) &&
+           (c->input_dtype == RSSM_F32 || c->input_dtype == RSSM_BF16) && c->tokens >= 1;
+}
+
+}  // namespace
+
+}  // namespace rssm
+
+extern "C" {
+
+RSSM_API size_t rssm_gdn_prefill_workspace_bytes(const rssm_gdn_prefill_config *cfg) {
+    return 0;
+}
+
+RSSM_API rssm_status rssm_gdn_prefill(const rssm_gdn_prefill_config *cfg, const float *S0, const rssm_inputs *in,
+                                      const int32_t *cu, float *y, float *S_out, void *workspace,
+                                      size_t workspace_bytes, int32_t *dev_error, void *stream) {
+    using namespace rssm;
+    if (!gdn_prefill_valid(cfg) || !in || !in->q || !in->k || !in->v || !in->alpha || !in->beta || !cu || !y || !S_out)
+        return RSSM_EINVAL;
+    if (S0 && S0 == S_out) return RSSM_EINVAL;
+    if (!aligned16(in->q) || !aligned16(in->k) || !aligned16(in->v) || !aligned16(y) || !aligned16(S_out) ||
+        !aligned16(S0))
+        return RSSM_EINVAL;
+    const size_t need = rssm_gdn_prefill_workspace_bytes(cfg);
+    if (need && (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 255))) return RSSM_EINVAL;
+    const rssm_gdn_prefill_config &c = *cfg;
+    const GdnPreArgs a{c.batch, c.nheads, c.headdim, c.tokens, in->q, in->k, in->v, in->alpha, in->beta,
+                       cu, S0, y, S_out, dev_error};
+    const cudaError_t e = c.input_dtype == RSSM_BF16 ? launch_recurrent<__nv_bfloat16>(a, c.dstate, (cudaStream_t)stream)
+                                                     : launch_recurrent<float>(a, c.dstate, (cudaStream_t)stream);
+    return e == cudaSuccess ? RSSM_OK : RSSM_ECUDA;
+}
+
+}  // extern "C"

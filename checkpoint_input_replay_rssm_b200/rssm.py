@@ -20,6 +20,7 @@ RSSM_MAMBA2, RSSM_GDN, RSSM_KDA = 0, 1, 2
 RSSM_REPLAY, RSSM_EAGER = 0, 1
 RSSM_F32, RSSM_BF16, RSSM_FP8E4M3 = 0, 1, 2
 RSSM_DEV_BAD_ACCEPT, RSSM_DEV_BAD_COUNTERS, RSSM_DEV_PIPE_TIMEOUT = 1, 2, 3
+RSSM_DEV_BAD_LENGTHS, RSSM_DEV_NO_PAGES, RSSM_DEV_BAD_PAGE = 4, 5, 6
 DTYPES = {"f32": RSSM_F32, "bf16": RSSM_BF16, "fp8": RSSM_FP8E4M3}
 KINDS = {"mamba2": RSSM_MAMBA2, "gdn": RSSM_GDN, "kda": RSSM_KDA}
 MODES = {"replay": RSSM_REPLAY, "eager": RSSM_EAGER}
@@ -50,10 +51,30 @@ class rssm_prefill_config(ctypes.Structure):
         "batch", "nheads", "headdim", "dstate", "ngroups", "T", "dt_scales_input")]
 
 
+class rssm_gdn_prefill_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("batch", "nheads", "headdim", "dstate", "input_dtype", "tokens")]
+
+
+class rssm_tables_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("batch", "page_size", "max_pages", "num_free", "max_tokens")]
+
+
+class rssm_kv4_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_kv_heads", "head_dim", "page_size", "num_pages")] + \
+               [(n, ctypes.c_float) for n in ("k_scale", "v_scale")]
+
+
+class rssm_attend_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("batch", "n_q_heads", "tokens", "max_pages", "max_q", "max_seq")] + \
+               [("sm_scale", ctypes.c_float)]
+
+
 # C declarations: name -> (restype, argtypes)
 _VP, _I32, _SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
 _CFGP, _LAYP, _INP = ctypes.POINTER(rssm_config), ctypes.POINTER(rssm_workspace_layout), ctypes.POINTER(rssm_inputs)
 _PCFGP = ctypes.POINTER(rssm_prefill_config)
+_GCFGP, _TCFGP = ctypes.POINTER(rssm_gdn_prefill_config), ctypes.POINTER(rssm_tables_config)
+_KCFGP, _ACFGP = ctypes.POINTER(rssm_kv4_config), ctypes.POINTER(rssm_attend_config)
 SIGNATURES = {
     "rssm_workspace_bytes": (_SZ, [_CFGP]),
     "rssm_workspace_layout_of": (ctypes.c_int, [_CFGP, _LAYP]),
@@ -75,6 +96,14 @@ SIGNATURES = {
     "rssm_launch_count": (ctypes.c_int64, [_VP]),
     "rssm_last_error": (ctypes.c_char_p, [_VP]),
     "rssm_mamba2_prefill": (ctypes.c_int, [_PCFGP, _VP, _VP, _VP, _INP, _VP, _VP, _VP, _VP]),
+    "rssm_gdn_prefill_workspace_bytes": (_SZ, [_GCFGP]),
+    "rssm_gdn_prefill": (ctypes.c_int, [_GCFGP, _VP, _INP, _VP, _VP, _VP, _VP, _SZ, _VP, _VP]),
+    "rssm_build_tables": (ctypes.c_int, [_TCFGP] + [_VP] * 12),
+    "rssm_kv4_cache_bytes": (_SZ, [_KCFGP]),
+    "rssm_kv4_append": (ctypes.c_int, [_KCFGP, _I32] + [_VP] * 6),
+    "rssm_kv4_export": (ctypes.c_int, [_KCFGP, _I32] + [_VP] * 6),
+    "rssm_kv4_attend_workspace_bytes": (_SZ, [_KCFGP, _ACFGP]),
+    "rssm_kv4_attend": (ctypes.c_int, [_KCFGP, _ACFGP] + [_VP] * 7 + [_SZ, _VP, _VP]),
 }
 
 _lib = None
@@ -229,6 +258,230 @@ def prefill(x, dt, Bm, Cm, A, D, S0=None, dt_scales_input=False, y=None, S_out=N
     rssm_mamba2_prefill(cfg, A.data_ptr(), D.data_ptr(), None if S0 is None else S0.data_ptr(), ins,
                         y.data_ptr(), S_out.data_ptr(), None if err is None else err.data_ptr(), st.cuda_stream)
     return y, S_out
+
+
+# ---------------------------------------------------------------- packed requests
+class _Call:
+    """Device and stream of one packed-request call: the tensors' device is current inside, and
+    what is allocated inside belongs to the stream that the kernels run on."""
+
+    def __init__(self, device, stream, *inputs):
+        import torch
+
+        self.torch, self.device, self.given = torch, device, stream
+        self.guard = torch.cuda.device(device) if torch.cuda.current_device() != device.index else None
+        self.inputs = inputs
+
+    def __enter__(self):
+        torch = self.torch
+        if self.guard is not None:
+            self.guard.__enter__()
+        self.ctx = None
+        if self.given is not None:
+            if self.given.device != self.device:
+                if self.guard is not None:
+                    self.guard.__exit__(None, None, None)
+                raise ValueError(f"the stream is on {self.given.device}, the tensors on {self.device}")
+            if self.given != torch.cuda.current_stream(self.device):
+                # tensors of another stream must not be handed out again before this one is done with them
+                for t in self.inputs:
+                    if t is not None:
+                        t.record_stream(self.given)
+            self.ctx = torch.cuda.stream(self.given)
+            self.ctx.__enter__()
+        return (self.given or torch.cuda.current_stream(self.device)).cuda_stream
+
+    def __exit__(self, *a):
+        if self.ctx is not None:
+            self.ctx.__exit__(*a)
+        if self.guard is not None:
+            self.guard.__exit__(*a)
+        return False
+
+
+def _want(name, t, dtype, shape, device):
+    """Pointer of a dense CUDA tensor of the given dtype, shape (None: any size) and device."""
+    if t.dtype != dtype or not t.is_cuda or t.device != device or not t.is_contiguous() or t.dim() != len(shape) \
+            or any(w is not None and w != n for w, n in zip(shape, t.shape)):
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape "
+                         f"{tuple('*' if w is None else w for w in shape)} on {device}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _opt(name, t, dtype, shape, device):
+    return None if t is None else _want(name, t, dtype, shape, device)
+
+
+def _cuda_device(t, name):
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor, got one on {t.device}")
+    return t.device
+
+
+def _ok(st, what):
+    if st != RSSM_OK:
+        raise RssmError(st, f"{what} refused its arguments" if st == RSSM_EINVAL else f"{what}: launch failed")
+
+
+def gdn_prefill(q, k, v, alpha, beta, cu_seqlens, S0=None, y=None, S_out=None, workspace=None, err=None,
+                stream=None):
+    """Torch convenience over rssm_gdn_prefill: the gated delta rule over packed prompts.
+
+    q, k [tokens, H, N], v [tokens, H, P] bf16 or fp32; alpha, beta [tokens, H] fp32; cu_seqlens
+    [B + 1] int32 row offsets of the prompts; S0 [B, H, P, N] fp32 or None (zero).  Returns
+    (y [tokens, H, P] fp32, S_out [B, H, P, N] fp32); S_out goes to ``Layer.import_state`` of a GDN
+    layer.  ``err`` (int32 [4], zeroed by the caller) receives device-side inconsistencies.
+    """
+    import torch
+
+    dev = _cuda_device(q, "q")
+    if q.dim() != 3 or v.dim() != 3 or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
+        raise ValueError("expected q, k, v of shape [tokens, heads, dim] and cu_seqlens of [requests + 1]")
+    T, H, N = q.shape
+    P, Bn = v.shape[2], cu_seqlens.shape[0] - 1
+    if q.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"q: expected bfloat16 or float32, got {q.dtype}")
+    f32, i32 = torch.float32, torch.int32
+    with _Call(dev, stream, q, k, v, alpha, beta, cu_seqlens, S0, y, S_out, workspace, err) as st:
+        y = torch.empty((T, H, P), dtype=f32, device=dev) if y is None else y
+        S_out = torch.empty((Bn, H, P, N), dtype=f32, device=dev) if S_out is None else S_out
+        cfg = rssm_gdn_prefill_config(Bn, H, P, N, RSSM_BF16 if q.dtype == torch.bfloat16 else RSSM_F32, T)
+        need = int(load().rssm_gdn_prefill_workspace_bytes(ctypes.byref(cfg)))
+        if need and workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        ins = rssm_inputs(q=_want("q", q, q.dtype, (T, H, N), dev), k=_want("k", k, q.dtype, (T, H, N), dev),
+                          v=_want("v", v, q.dtype, (T, H, P), dev), alpha=_want("alpha", alpha, f32, (T, H), dev),
+                          beta=_want("beta", beta, f32, (T, H), dev))
+        _ok(load().rssm_gdn_prefill(
+            ctypes.byref(cfg), _opt("S0", S0, f32, (Bn, H, P, N), dev), ctypes.byref(ins),
+            _want("cu_seqlens", cu_seqlens, i32, (Bn + 1,), dev), _want("y", y, f32, (T, H, P), dev),
+            _want("S_out", S_out, f32, (Bn, H, P, N), dev), _opt("workspace", workspace, torch.uint8, (None,), dev),
+            0 if workspace is None else workspace.shape[0], _opt("err", err, i32, (4,), dev), st), "rssm_gdn_prefill")
+    return y, S_out
+
+
+def build_tables(cached_len, new_len, free_pages, free_head, block_table, page_size, max_tokens, err=None,
+                 stream=None):
+    """Torch convenience over rssm_build_tables (all int32): block_table [B, max_pages] is updated in
+    place with pages of free_pages from entry free_head [1] on; returns (cu_new [B + 1], seq_len [B],
+    slot_map [max_tokens], position [max_tokens], next_free [1])."""
+    import torch
+
+    dev, i32 = _cuda_device(cached_len, "cached_len"), torch.int32
+    if cached_len.dim() != 1 or block_table.dim() != 2 or free_pages.dim() != 1:
+        raise ValueError("expected cached_len [requests], block_table [requests, pages] and free_pages [pages]")
+    Bn, width = cached_len.shape[0], block_table.shape[1]
+    with _Call(dev, stream, cached_len, new_len, free_pages, free_head, block_table, err) as st:
+        # one allocation for the five results, each on a 16-byte boundary
+        sizes = (Bn + 1, Bn, max_tokens, max_tokens, 1)
+        at = [0]
+        for n in sizes:
+            at.append(at[-1] + (max(n, 1) + 3 & ~3))
+        buf = torch.empty(at[-1], dtype=i32, device=dev)
+        out = tuple(buf[a:a + n] for a, n in zip(at, sizes))
+        base = buf.data_ptr()
+        cfg = rssm_tables_config(Bn, page_size, width, free_pages.shape[0], max_tokens)
+        _ok(load().rssm_build_tables(
+            ctypes.byref(cfg), _want("cached_len", cached_len, i32, (Bn,), dev),
+            _want("new_len", new_len, i32, (Bn,), dev), _want("free_pages", free_pages, i32, (None,), dev),
+            _want("free_head", free_head, i32, (1,), dev), _want("block_table", block_table, i32, (Bn, width), dev),
+            *(base + 4 * a for a in at[:5]), _opt("err", err, i32, (4,), dev), st), "rssm_build_tables")
+    return out
+
+
+def kv4_cache(num_pages, n_kv_heads, page_size, head_dim, device="cuda"):
+    """A zeroed paged 4-bit key/value cache: uint8 [num_pages, n_kv_heads, page_size * head_dim * 9 / 8]."""
+    import torch
+
+    cfg = rssm_kv4_config(n_kv_heads, head_dim, page_size, num_pages, 1.0, 1.0)
+    if not load().rssm_kv4_cache_bytes(ctypes.byref(cfg)):
+        raise RssmError(RSSM_EINVAL, "no 4-bit cache of these sizes: head_dim is 64 or 128, page_size a multiple of "
+                                     "16 up to 256, num_pages * page_size < 2^31")
+    return torch.zeros((num_pages, n_kv_heads, page_size * head_dim * 9 // 8), dtype=torch.uint8, device=device)
+
+
+def _kv4_config(cache, head_dim, k_scale, v_scale):
+    import torch
+
+    if cache.dtype != torch.uint8 or cache.dim() != 3 or not cache.is_cuda or not cache.is_contiguous():
+        raise ValueError("cache: expected a contiguous CUDA uint8 tensor [pages, kv heads, page bytes]")
+    pages, heads, nb = cache.shape
+    ps = nb * 8 // (9 * head_dim)
+    if ps * 9 * head_dim != nb * 8:
+        raise ValueError(f"cache: {nb} bytes a page and head are no whole number of tokens of {head_dim} channels")
+    return rssm_kv4_config(heads, head_dim, ps, pages, k_scale, v_scale)
+
+
+def kv4_append(k, v, slot_map, cache, k_scale=1.0, v_scale=1.0, err=None, stream=None):
+    """Torch convenience over rssm_kv4_append: write k, v [tokens, kv heads, head_dim] bf16 to the
+    slots slot_map [tokens] int32 (negative: skipped) of ``cache`` (``kv4_cache``), in place."""
+    import torch
+
+    if k.dim() != 3 or cache.dim() != 3:
+        raise ValueError("expected k of shape [tokens, kv heads, head_dim] and cache of [pages, kv heads, bytes]")
+    dev, (T, _, D), bf = _cuda_device(k, "k"), k.shape, torch.bfloat16
+    cfg = _kv4_config(cache, D, k_scale, v_scale)
+    sh = (T, cache.shape[1], D)
+    with _Call(dev, stream, k, v, slot_map, cache, err) as st:
+        _ok(load().rssm_kv4_append(
+            ctypes.byref(cfg), T, _want("k", k, bf, sh, dev), _want("v", v, bf, sh, dev),
+            _want("slot_map", slot_map, torch.int32, (T,), dev), _want("cache", cache, torch.uint8, cache.shape, dev),
+            _opt("err", err, torch.int32, (4,), dev), st), "rssm_kv4_append")
+
+
+def kv4_export(slot_map, cache, head_dim, k_scale=1.0, v_scale=1.0, k=None, v=None, err=None, stream=None):
+    """Torch convenience over rssm_kv4_export: the values held at slot_map [tokens] as bf16
+    (k, v) [tokens, kv heads, head_dim]."""
+    import torch
+
+    dev, bf = _cuda_device(slot_map, "slot_map"), torch.bfloat16
+    if cache.dim() != 3 or slot_map.dim() != 1:
+        raise ValueError("expected slot_map of shape [tokens] and cache of [pages, kv heads, bytes]")
+    cfg = _kv4_config(cache, head_dim, k_scale, v_scale)
+    T = slot_map.shape[0]
+    sh = (T, cache.shape[1], head_dim)
+    with _Call(dev, stream, slot_map, cache, k, v, err) as st:
+        k = torch.empty(sh, dtype=bf, device=dev) if k is None else k
+        v = torch.empty(sh, dtype=bf, device=dev) if v is None else v
+        _ok(load().rssm_kv4_export(
+            ctypes.byref(cfg), T, _want("slot_map", slot_map, torch.int32, (T,), dev),
+            _want("cache", cache, torch.uint8, cache.shape, dev), _want("k", k, bf, sh, dev),
+            _want("v", v, bf, sh, dev), _opt("err", err, torch.int32, (4,), dev), st), "rssm_kv4_export")
+    return k, v
+
+
+def kv4_attend(q, cache, block_table, seq_len, cu_q, max_q, k_scale=1.0, v_scale=1.0, sm_scale=None, max_seq=None,
+               out=None, workspace=None, err=None, stream=None):
+    """Torch convenience over rssm_kv4_attend: causal attention of q [tokens, query heads, head_dim]
+    bf16 over the cached tokens of each request (its own appended first), the requests packed by
+    cu_q [B + 1] int32 with at most max_q rows each, seq_len [B] int32 cached tokens found through
+    block_table [B, max_pages] int32.  sm_scale defaults to head_dim ** -0.5, max_seq (a bound of
+    seq_len that sizes the launch) to max_pages * page_size.  Returns out [tokens, query heads,
+    head_dim] bf16."""
+    import torch
+
+    if q.dim() != 3 or cache.dim() != 3 or block_table.dim() != 2 or seq_len.dim() != 1:
+        raise ValueError("expected q [tokens, heads, head_dim], cache [pages, kv heads, bytes], block_table "
+                         "[requests, pages] and seq_len [requests]")
+    dev, (T, Hq, D), bf, i32 = _cuda_device(q, "q"), q.shape, torch.bfloat16, torch.int32
+    cfg = _kv4_config(cache, D, k_scale, v_scale)
+    Bn, width = block_table.shape
+    att = rssm_attend_config(Bn, Hq, T, width, max_q, width * cfg.page_size if max_seq is None else max_seq,
+                             D ** -0.5 if sm_scale is None else sm_scale)
+    with _Call(dev, stream, q, cache, block_table, seq_len, cu_q, out, workspace, err) as st:
+        out = torch.empty((T, Hq, D), dtype=bf, device=dev) if out is None else out
+        need = int(load().rssm_kv4_attend_workspace_bytes(ctypes.byref(cfg), ctypes.byref(att)))
+        if need and workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        _ok(load().rssm_kv4_attend(
+            ctypes.byref(cfg), ctypes.byref(att), _want("q", q, bf, (T, Hq, D), dev),
+            _want("cache", cache, torch.uint8, cache.shape, dev),
+            _want("block_table", block_table, i32, (Bn, width), dev), _want("seq_len", seq_len, i32, (Bn,), dev),
+            _want("cu_q", cu_q, i32, (Bn + 1,), dev), _want("out", out, bf, (T, Hq, D), dev),
+            _opt("workspace", workspace, torch.uint8, (None,), dev), 0 if workspace is None else workspace.shape[0],
+            _opt("err", err, i32, (4,), dev), st), "rssm_kv4_attend")
+    return out
 
 
 # ---------------------------------------------------------------- torch owner

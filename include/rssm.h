@@ -89,8 +89,11 @@ typedef enum {
     RSSM_DEV_BAD_COUNTERS = 2, /* seq_pos - ckpt_pos outside [0, window], or a fold due that the
                                   host did not schedule (counters changed outside the API);
                                   sequence skipped */
-    RSSM_DEV_PIPE_TIMEOUT = 3  /* a bulk copy into shared memory did not complete within 2 s;
+    RSSM_DEV_PIPE_TIMEOUT = 3, /* a bulk copy into shared memory did not complete within 2 s;
                                   the kernel stopped and the sequence was left as it was */
+    RSSM_DEV_BAD_LENGTHS = 4,  /* request lengths or packed offsets that do not fit the call's sizes */
+    RSSM_DEV_NO_PAGES = 5,     /* the free list holds fewer pages than the requests need */
+    RSSM_DEV_BAD_PAGE = 6      /* a page or slot outside the cache; it was neither read nor written */
 } rssm_device_error;
 
 typedef struct {
@@ -255,6 +258,125 @@ typedef struct {
 RSSM_API rssm_status rssm_mamba2_prefill(const rssm_prefill_config *cfg, const float *A, const float *D,
                                          const float *S0, const rssm_inputs *in, float *y, float *S_out,
                                          int32_t *dev_error, void *stream);
+
+/* ---- Packed requests --------------------------------------------------------------------
+ * The calls below work on requests of different lengths laid one after another: request b
+ * owns the rows cu[b] .. cu[b+1] - 1 of every token array (cu: int32[B+1], cu[0] >= 0, not
+ * descending).  They hold no handle: each takes its sizes in a config, enqueues on `stream`
+ * (a cudaStream_t on the current device, NULL = legacy default stream), allocates nothing and
+ * does not synchronise, so each can be captured in a graph.  Two calls in flight may share
+ * inputs but not outputs or workspace.  `dev_error` (device int32[4] or NULL) receives
+ * {code, request, head, value} of the first inconsistency that only the device can see and is
+ * otherwise left alone; the caller zeroes it.  Host-visible misuse is RSSM_EINVAL with nothing
+ * enqueued. */
+
+/* The gated delta rule over packed prompts: for every request b and head h, run its tokens
+ * through S_t = alpha_t S_{t-1} (I - beta_t k_t k_t^T) + beta_t v_t k_t^T, o_t = S_t q_t from
+ * the state S0 and write every token's output and the fp32 state after the prompt, to be
+ * installed with rssm_import_state (the prompt step of a Gated DeltaNet layer, as
+ * rssm_mamba2_prefill is of a Mamba-2 layer; the pages on checkpointed input replay describe
+ * no prefill).  A request of no tokens copies its S0.
+ *   cfg:   batch (1..65535), nheads (1..65535), headdim P and dstate N as for rssm_config,
+ *          input_dtype F32 | BF16, tokens = rows of the token arrays (>= 1).
+ *   S0:    device fp32 [B][H][P][N], or NULL for a zero state.
+ *   in:    q, k [tokens][H][N], v [tokens][H][P] in input_dtype, alpha (>= 0), beta
+ *          [tokens][H] fp32; the other fields are ignored.
+ *   cu:    device int32[B+1] as above, cu[B] <= tokens.
+ *   y:     device fp32 [tokens][H][P]; rows of no request are left as they were.
+ *   S_out: device fp32 [B][H][P][N] (may not alias S0).
+ *   workspace: device, 256-byte aligned, rssm_gdn_prefill_workspace_bytes(cfg) bytes (NULL
+ *          where that is 0).
+ * A request whose offsets are out of order or out of range sets RSSM_DEV_BAD_LENGTHS and is
+ * skipped (its rows of y and S_out are left as they were). */
+typedef struct {
+    int32_t batch, nheads, headdim, dstate;
+    int32_t input_dtype; /* F32 | BF16 */
+    int32_t tokens;      /* rows of q, k, v, alpha, beta and y */
+} rssm_gdn_prefill_config;
+RSSM_API size_t rssm_gdn_prefill_workspace_bytes(const rssm_gdn_prefill_config *cfg);
+RSSM_API rssm_status rssm_gdn_prefill(const rssm_gdn_prefill_config *cfg, const float *S0, const rssm_inputs *in,
+                                      const int32_t *cu, float *y, float *S_out, void *workspace,
+                                      size_t workspace_bytes, int32_t *dev_error, void *stream);
+
+/* Block table, slot map and packed offsets of one step, from the requests' lengths.  Request
+ * b holds cached_len[b] tokens in the first ceil(cached_len[b] / page_size) entries of its
+ * row of block_table and adds new_len[b] >= 0 tokens.  The pages it lacks are taken from
+ * free_pages in order (request by request) from entry *free_head on and written behind the
+ * ones it holds; the other entries of the row are left as they were.
+ *   cfg:        batch 1..16384; page_size 1..65536; max_pages = row length of block_table;
+ *               num_free = entries of free_pages; max_tokens = rows of slot_map and position
+ *               (both at most 2^30).
+ *   cu_new:     int32[B+1] packed offsets of the new tokens.
+ *   seq_len:    int32[B] cached_len + new_len.
+ *   slot_map:   int32[max_tokens] slot of every new token, page * page_size + offset.
+ *   position:   int32[max_tokens] its position in its request.  Rows behind the last new
+ *               token hold -1 in both.
+ *   next_free:  int32: *free_head plus the pages taken (may not alias free_head).
+ * Lengths that are negative or exceed max_pages * page_size, more new tokens than max_tokens
+ * (RSSM_DEV_BAD_LENGTHS) or more pages than the list holds (RSSM_DEV_NO_PAGES) refuse the
+ * whole step: the table is left as it was, no page is taken, cu_new is 0, seq_len is
+ * cached_len and every slot and position is -1.  A table entry below 0 gives slot -1. */
+typedef struct {
+    int32_t batch, page_size, max_pages, num_free, max_tokens;
+} rssm_tables_config;
+RSSM_API rssm_status rssm_build_tables(const rssm_tables_config *cfg, const int32_t *cached_len,
+                                       const int32_t *new_len, const int32_t *free_pages, const int32_t *free_head,
+                                       int32_t *block_table, int32_t *cu_new, int32_t *seq_len, int32_t *slot_map,
+                                       int32_t *position, int32_t *next_free, int32_t *dev_error, void *stream);
+
+/* A paged key/value cache held in 4 bits, for the attention layers of a hybrid model.
+ * cache: uint8 [num_pages][n_kv_heads][page_size * head_dim * 9 / 8]; the bytes of one page
+ * and head are the K codes [page_size][head_dim / 2] (element 2i in the low half of byte i),
+ * the K block scales [page_size][head_dim / 16], then V's codes and scales.  A code is e2m1, a
+ * block scale e4m3 over 16 consecutive elements, and a held value is code * block scale *
+ * tensor scale.  Writing x: block scale = e4m3(max|x| / (6 tensor scale)), code = e2m1(x /
+ * (block scale * tensor scale)), both round to nearest even and saturate; an infinity becomes
+ * the largest value, a block with a NaN holds NaN.  The tensor scales are powers of two (the
+ * block scale carries the mantissa), so every held value is a bf16 number wherever it is in
+ * bf16's range.
+ *   cfg: head_dim 64 or 128; page_size a multiple of 16, 16..256; num_pages * page_size
+ *        < 2^31; k_scale, v_scale powers of two in 2^-64..2^64. */
+typedef struct {
+    int32_t n_kv_heads, head_dim, page_size, num_pages;
+    float k_scale, v_scale;
+} rssm_kv4_config;
+/* Bytes of the cache (0 if cfg is invalid). */
+RSSM_API size_t rssm_kv4_cache_bytes(const rssm_kv4_config *cfg);
+
+/* Write `tokens` rows of k and v (device bf16 [tokens][n_kv_heads][head_dim]) to the slots
+ * slot_map[t].  A negative slot is skipped; one past the cache sets RSSM_DEV_BAD_PAGE.  Slots
+ * of one call are distinct (of two rows with one slot, either or a mixture of blocks stays). */
+RSSM_API rssm_status rssm_kv4_append(const rssm_kv4_config *cfg, int32_t tokens, const void *k, const void *v,
+                                     const int32_t *slot_map, void *cache, int32_t *dev_error, void *stream);
+/* The values held at the given slots as bf16 [tokens][n_kv_heads][head_dim] each; a row whose
+ * slot is negative or past the cache (RSSM_DEV_BAD_PAGE) is zero. */
+RSSM_API rssm_status rssm_kv4_export(const rssm_kv4_config *cfg, int32_t tokens, const int32_t *slot_map,
+                                     const void *cache, void *k, void *v, int32_t *dev_error, void *stream);
+
+/* Causal grouped-query attention over the cache, for one decode token, the drafts of a verify
+ * or the chunk of a prompt: query row i of request b's n = cu_q[b+1] - cu_q[b] rows sees the
+ * first seq_len[b] - n + i + 1 cached tokens (its own among them: append comes first) and gets
+ * out = softmax(sm_scale q K^T) V; a row that sees none gets 0.  Query head j reads key/value
+ * head j / (n_q_heads / n_kv_heads).  Scores, softmax and sums are fp32.
+ *   batch 1..65535, n_q_heads a multiple of n_kv_heads, tokens = rows of q and out,
+ *   max_pages = row length of block_table (int32 [B][max_pages]), max_q >= every n,
+ *   max_seq >= every seq_len (both size the launch, so that it can be captured once for
+ *   growing requests).  q, out: device bf16 [tokens][n_q_heads][head_dim]; rows of no request
+ *   are left as they were.
+ *   workspace: device, 256-byte aligned, rssm_kv4_attend_workspace_bytes bytes (NULL where 0).
+ * A request whose offsets or length do not fit (cu_q out of order or past tokens, n > max_q,
+ * seq_len < 0, > max_seq or > max_pages * page_size) sets RSSM_DEV_BAD_LENGTHS and its rows
+ * are left as they were; a page outside the cache sets RSSM_DEV_BAD_PAGE and its tokens are
+ * left out as if masked. */
+typedef struct {
+    int32_t batch, n_q_heads, tokens, max_pages, max_q, max_seq;
+    float sm_scale;
+} rssm_attend_config;
+RSSM_API size_t rssm_kv4_attend_workspace_bytes(const rssm_kv4_config *cfg, const rssm_attend_config *att);
+RSSM_API rssm_status rssm_kv4_attend(const rssm_kv4_config *cfg, const rssm_attend_config *att, const void *q,
+                                     const void *cache, const int32_t *block_table, const int32_t *seq_len,
+                                     const int32_t *cu_q, void *out, void *workspace, size_t workspace_bytes,
+                                     int32_t *dev_error, void *stream);
 
 /* Speculative verify of K drafts (1 <= K <= max_draft, K <= W) for every
  * sequence: folds where len + K > W, appends the drafts uncommitted and writes
