@@ -1,16 +1,37 @@
 // rssm_kv4_attend.cu -- causal grouped-query attention over the paged 4-bit cache
-// (rssm_kv4_attend).
+// (rssm_kv4_attend), for one decode token, the drafts of a verify or a prompt chunk.
 //
-//   out = sum_j p_j V_j / sum_j p_j,  p_j = exp(sm_scale q . K_j - m),  m the running maximum
+//   out = sum_j p_j V_j / sum_j p_j,  p_j = 2^{s_j - m},  s_j = sm_scale log2(e) q . K_j
 //
-// One CTA per (query row, query head); its warps take the cached tokens in turn, a
-// lane holding D / 32 channels, and join their (m, sum, O) at the end.
+// The cache is read once per tile of 16 or 32 query rows (a request's rows times the
+// query heads of one key/value head).  At 0.56 bytes an element the work that
+// dequantising asks for is next to the bytes what bounds the kernel, so the codes go from
+// shared memory to matrix-instruction operands inside a thread's registers and are
+// never written back wide.  What makes that possible is that the channel order of
+// the first product and the token order of the second are free, as long as both
+// operands agree:
+//   scores: lane (g, c) holds token g's channels [c D/4, (c+1) D/4), a 16-byte run of
+//           codes with two block scales; k-step s multiplies its channels 4s .. 4s+3.
+//   output: lane (r, c) holds the 16 (D = 64: 8) channels of block r of four tokens;
+//           column r of n-tile j is channel j of block r.  Operands pair two tokens, so
+//           the two tokens' nibbles are merged before they are widened.
+// e2m1 x e4m3 has 6 significant bits, so the fp16 operands are exact.  Queries are scaled
+// by a power of two per row (their bf16 bits fit fp16, smaller than 2^-33 of the row's
+// largest is dropped); probabilities are fp16 (2^-11 of each), their sums, the
+// running maximum and the accumulators fp32.  m trails the true maximum by up to
+// 2^6, so that the accumulators are rescaled a few times per row and not each step.
+//
+// A warp streams its own tokens: 32 at a time, every kWarps-th group of 32 of the
+// CTA's range, by bulk copies into a ring of kStages stages of its own; the warps of a CTA meet
+// only at the end, to join their sums.  Long contexts are split over CTAs and
+// joined by a second kernel.
 #include <cuda_bf16.h>
 
 #include <math.h>
 
 #include "rssm_internal.h"
 #include "rssm_kv4.cuh"
+#include "rssm_pipe.cuh"
 
 namespace rssm {
 
@@ -18,13 +39,36 @@ namespace {
 
 struct AttendArgs {
     Kv4Args kv;
-    int B, Hq, tokens, max_pages, max_q, max_seq;
-    float scale;
+    int B, Hq, G, tokens, max_pages, max_q, max_seq;
+    int tiles, splits, L;  // row tiles a request, splits, cached tokens a split
+    float scale;           // sm_scale * k_scale * log2(e)
     const __nv_bfloat16 *q;
     const uint8_t *cache;
     const int32_t *table, *seq_len, *cu;
     __nv_bfloat16 *out;
+    float *part;  // [B][Hk][tiles][splits][rows][D], then (m, l) [...][rows][2]
     int32_t *err;
+};
+
+constexpr int kWarps4 = 4;
+constexpr int kStages = 4;
+constexpr int kStep = 32;        // tokens a warp takes at a time
+constexpr float kLag = 6.f;      // log2 by which the running maximum may trail
+
+template <int D> struct Ring {
+    static constexpr int kGran = 16 * D * 9 / 8;           // 16 tokens: K codes, K scales, V codes, V scales
+    static constexpr int kPad = D == 128 ? 32 : 64;        // the second 16 tokens' rows fall into the other banks
+    static constexpr int kStage = 2 * (kGran + kPad);
+    static constexpr int kScale = 16 * D / 2;              // scales behind codes
+    static constexpr int kV = 16 * D * 9 / 16;             // values behind keys
+};
+template <int D, int MT> struct Smem {
+    static constexpr int kRing = kWarps4 * kStages * Ring<D>::kStage;
+    static constexpr int kMerge = kWarps4 * 16 * (D + 4) * 4;  // over the ring, one 16-row tile at a time
+    static constexpr int kQ = kRing > kMerge ? kRing : kMerge;
+    static constexpr int kMl = kQ + MT * (D / 16) * 512;       // query operands: [mt][k-step][lane] 16 bytes
+    static constexpr int kBar = kMl + kWarps4 * MT * 16 * 8;   // (m, l) of every warp and row
+    static constexpr int kBytes = kBar + kWarps4 * kStages * 8;
 };
 
 // The rows and length of request b; false (and reported) where they do not fit the call.
@@ -36,85 +80,539 @@ __device__ __forceinline__ bool attend_request(const AttendArgs &a, int b, int &
     return ok && n <= a.max_q && len >= 0 && len <= a.max_seq && len <= (int64_t)a.max_pages * a.kv.ps;
 }
 
-constexpr int kAttWarps = 4;
-
-__device__ __forceinline__ float e2m1_value(uint32_t c) {
-    const float m = (c & 6) == 0 ? 0.5f * (c & 1) : ldexpf(1.f + 0.5f * (c & 1), (int)((c >> 1) & 3) - 1);
-    return (c & 8) ? -m : m;
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
 }
-__device__ __forceinline__ float e4m3_f(uint32_t b) {
-    return __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)b, __NV_E4M3)));
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+// The four bytes of w, two e2m1 codes each, as fp16 pairs.
+__device__ __forceinline__ void widen(uint32_t w, uint32_t (&h)[4]) {
+    asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %4;\n cvt.rn.f16x2.e2m1x2 %0, a;\n"
+        " cvt.rn.f16x2.e2m1x2 %1, b;\n cvt.rn.f16x2.e2m1x2 %2, c;\n cvt.rn.f16x2.e2m1x2 %3, d;\n}\n"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(w));
+}
+// Two e4m3 bytes (low 16 bits of w) as an fp16 pair.
+__device__ __forceinline__ uint32_t scales2(uint32_t w) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)w));
+    return r;
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <int D>
-__global__ void __launch_bounds__(32 * kAttWarps) attend_rows_kernel(const AttendArgs a) {
-    constexpr int E = D / 32;
-    __shared__ float so[kAttWarps][D], sm[kAttWarps], sl[kAttWarps];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int i = blockIdx.x, hq = blockIdx.y, b = blockIdx.z;
+// A row's power-of-two scale: the largest magnitude goes to [2^9, 2^10).
+__device__ __forceinline__ int row_exponent(float top) {
+    if (!(top > 0.f) || top > 3.4e38f) return 0;
+    int e;
+    frexpf(top, &e);
+    return e - 10;
+}
+
+template <int D, int MT>
+__global__ void __launch_bounds__(32 * kWarps4, MT == 1 ? 3 : 2) attend_kernel(const AttendArgs a) {
+    using R = Ring<D>;
+    using S = Smem<D, MT>;
+    constexpr int KS = D / 16;   // k-steps of the scores
+    constexpr int NT = D / 8;    // n-tiles of the output
+    constexpr int RT = 16 * MT;  // rows of the tile
+    extern __shared__ __align__(128) uint8_t sm[];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
+    const int split = blockIdx.x, tile = blockIdx.y % a.tiles, h = blockIdx.y / a.tiles, b = blockIdx.z;
+    const int ps = a.kv.ps, G = a.G;
     int r0, n, len;
     if (!attend_request(a, b, r0, n, len)) {
-        if (threadIdx.x == 0) report_opt(a.err, DEV_BAD_LENGTHS, b, 0, len);
+        if (tid == 0) report_opt(a.err, DEV_BAD_LENGTHS, b, 0, len);
         return;
     }
-    if (i >= n) return;
-    const int seen = len - n + i + 1, h = hq / (a.Hq / a.kv.Hk), ps = a.kv.ps;
-    const int64_t at = ((int64_t)(r0 + i) * a.Hq + hq) * D + lane * E;
-    float q[E], o[E] = {}, m = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) q[e] = __bfloat162float(a.q[at + e]) * a.scale;
-    for (int t = warp; t < seen; t += kAttWarps) {
-        const int page = a.table[(int64_t)b * a.max_pages + t / ps], off = t % ps;
-        if (page < 0 || page >= a.kv.pages) {
-            if (lane == 0) report_opt(a.err, DEV_BAD_PAGE, b, h, page);
-            continue;
-        }
-        const uint8_t *kb = a.cache + ((int64_t)page * a.kv.Hk + h) * kv4_head_bytes(ps, D), *vb = kb + ps * (D * 9 / 16);
-        const float ks = e4m3_f(kb[ps * (D / 2) + off * (D / 16) + lane * E / 16]) * a.kv.k_scale;
-        const float vs = e4m3_f(vb[ps * (D / 2) + off * (D / 16) + lane * E / 16]) * a.kv.v_scale;
-        float s = 0.f, v[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const int byte = off * (D / 2) + (lane * E + e) / 2, sh = 4 * (e & 1);
-            s = fmaf(q[e], e2m1_value((kb[byte] >> sh) & 15) * ks, s);
-            v[e] = e2m1_value((vb[byte] >> sh) & 15) * vs;
-        }
-#pragma unroll
-        for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-        const float mn = fmaxf(m, s), c = expf(m - mn), p = expf(s - mn);
-        l = l * c + p;
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = o[e] * c + p * v[e];
-        m = mn;
-    }
-#pragma unroll
-    for (int e = 0; e < E; ++e) so[warp][lane * E + e] = o[e];
+    const int rows = n * G, row0 = tile * RT;
+    if (row0 >= rows) return;
+    // tokens that the tile's last row sees
+    const int last = min(row0 + RT, rows) - 1;
+    const int tlen = max(0, len - n + last / G + 1);
+    const int ns = max(1, (tlen + a.L - 1) / a.L);
+    if (split >= ns) return;
+    const int t_begin = split * a.L, t_end = min(tlen, t_begin + a.L);
+    const int first_seen = len - n + row0 / G + 1;  // tokens that the tile's first row sees
+
+    uint8_t *ring = sm + warp * kStages * R::kStage;
+    uint4 *sq = reinterpret_cast<uint4 *>(sm + S::kQ);
+    float2 *sml = reinterpret_cast<float2 *>(sm + S::kMl);
+    uint64_t *bar = reinterpret_cast<uint64_t *>(sm + S::kBar) + warp * kStages;
     if (lane == 0) {
-        sm[warp] = m;
-        sl[warp] = l;
+#pragma unroll
+        for (int s = 0; s < kStages; ++s) mbar_init(bar + s, 1);
+        mbar_init_fence();
+    }
+    __syncwarp();
+
+    // This warp's steps: tokens t_begin + 32 (warp + kWarps4 i).  Lane l keeps the page of
+    // 16-token group l & 1 of step l >> 1 of a window of 16 steps, -1 for one that is not
+    // read (behind the last token, or outside the cache).
+    const int steps_all = (max(0, t_end - t_begin) + kStep - 1) / kStep;
+    const int steps = steps_all > warp ? (steps_all - warp + kWarps4 - 1) / kWarps4 : 0;
+    auto pages_of = [&](int win) {
+        const int i = win * 16 + (lane >> 1);
+        const int t = t_begin + kStep * (warp + kWarps4 * i) + 16 * (lane & 1);
+        int page = -1;
+        if (i < steps && t < t_end) {
+            page = a.table[(int64_t)b * a.max_pages + t / ps];
+            if (page < 0 || page >= a.kv.pages) {
+                report_opt(a.err, DEV_BAD_PAGE, b, h, page);
+                page = -1;
+            }
+        }
+        return page;
+    };
+    int pg = pages_of(0), pg_next = pages_of(1);
+    const int64_t head_bytes = kv4_head_bytes(ps, D);
+    // Start the copies of step i: lane 4 gr + piece copies that piece of 16-token group gr.
+    auto issue = [&](int i, int window) {
+        const int gr = (lane >> 2) & 1, piece = lane & 3;
+        const int pw = (i >> 4) == window ? pg : pg_next;
+        const int page = __shfl_sync(0xffffffffu, pw, 2 * (i & 15) + gr);
+        const int other = __shfl_xor_sync(0xffffffffu, page, 4);
+        uint64_t *br = bar + i % kStages;
+        if (lane == 0) mbar_arrive_expect_tx(br, R::kGran * ((page >= 0) + (other >= 0)));
+        __syncwarp();
+        if (lane < 8 && page >= 0 && (piece == 0 || ps != 16)) {
+            const int off = (t_begin + kStep * (warp + kWarps4 * i) + 16 * gr) % ps;
+            const uint8_t *src = a.cache + ((int64_t)page * a.kv.Hk + h) * head_bytes;
+            uint8_t *dst = ring + (i % kStages) * R::kStage + gr * (R::kGran + R::kPad);
+            if (ps == 16) {  // a page is laid out as a group is
+                bulk_g2s(dst, src, R::kGran, br);
+            } else {
+                const bool sc = piece & 1, v = piece & 2;
+                src += (v ? ps * (D * 9 / 16) : 0) + (sc ? ps * (D / 2) + off * (D / 16) : off * (D / 2));
+                bulk_g2s(dst + (v ? R::kV : 0) + (sc ? R::kScale : 0), src, sc ? D : R::kScale, br);
+            }
+        }
+    };
+    for (int i = 0; i < kStages - 1 && i < steps; ++i) issue(i, 0);
+
+    // Query operands of the tile's rows, made by the warps in turn: [mt][k-step][lane].
+    float f[MT][2];   // factor of this lane's rows' scores
+    int seen[MT][2];  // tokens that they see
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        uint32_t w[2][KS][2];  // [row][k-step][channels 0-1, 2-3 of the step's four]
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int row = row0 + 16 * mt + g + 8 * u;
+            const bool live = row < rows;
+            const int i = live ? row / G : 0, hd = live ? row - i * G : 0;
+            seen[mt][u] = live ? len - n + i + 1 : 0;
+            const uint4 *src = reinterpret_cast<const uint4 *>(
+                a.q + ((int64_t)(r0 + i) * a.Hq + h * G + hd) * D + c * (D / 4));
+            uint4 raw[D / 32];
+            float top = 0.f;
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) {
+                raw[k] = live ? src[k] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t x = (&raw[k].x)[e];
+                    top = fmaxf(top, fmaxf(fabsf(bf16_bits_to_float(x & 0xffff)), fabsf(bf16_bits_to_float(x >> 16))));
+                }
+            }
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const int ex = row_exponent(top);
+            // 2^-ex as two factors: one alone may leave fp32's range
+            const float s0 = ldexpf(1.f, -(ex / 2)), s1 = ldexpf(1.f, -(ex - ex / 2));
+            f[mt][u] = ldexpf(a.scale, ex);
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t x = (&raw[k].x)[e];
+                    w[u][2 * k + (e >> 1)][e & 1] = f16x2(bf16_bits_to_float(x & 0xffff) * s0 * s1,
+                                                          bf16_bits_to_float(x >> 16) * s0 * s1);
+                }
+        }
+        if (warp == mt % kWarps4)
+#pragma unroll
+            for (int s = 0; s < KS; ++s)
+                sq[(mt * KS + s) * 32 + lane] = make_uint4(w[0][s][0], w[1][s][0], w[0][s][1], w[1][s][1]);
     }
     __syncthreads();
-    if (warp) return;
-    float mm = -INFINITY, ll = 0.f;
-    for (int w = 0; w < kAttWarps; ++w) mm = fmaxf(mm, sm[w]);
+
+    float o[MT][NT][4], m[MT][2], l[MT][2];
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = 0.f;
-    for (int w = 0; w < kAttWarps; ++w) {
-        const float c = sm[w] == -INFINITY ? 0.f : expf(sm[w] - mm);
-        ll += c * sl[w];
+    for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] += c * so[w][lane * E + e];
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[mt][j][e] = 0.f;
+        m[mt][0] = m[mt][1] = -INFINITY;
+        l[mt][0] = l[mt][1] = 0.f;
+    }
+
+    // Token of a step: group (16), then 4 x n-tile + 2 e + (e ^ parity), so that neighbouring lanes of either
+    // product's loads read rows an odd number apart (no bank conflicts).
+    const int ge = g & 1, gc = (g >> 1) & 1;
+    const int k_at = (g >> 2) * (R::kGran + R::kPad) + (2 * ge + (ge ^ gc)) * (D / 2) + c * (D / 8);
+    const int ks_at = (g >> 2) * (R::kGran + R::kPad) + R::kScale + (2 * ge + (ge ^ gc)) * (D / 16) + c * (D / 64);
+    const int v_at = (c >> 1) * (R::kGran + R::kPad) + R::kV + g * (D / 16);
+    const int vs_at = (c >> 1) * (R::kGran + R::kPad) + R::kV + R::kScale + (D == 128 ? g : g >> 1);
+    const int par = c & 1;
+
+    bool failed = false;
+    for (int i = 0; i < steps; ++i) {
+        const int window = i >> 4;
+        if ((i & 15) == 0 && i > 0) {
+            pg = pg_next;
+            pg_next = pages_of(window + 1);
+        }
+        if (i + kStages - 1 < steps) issue(i + kStages - 1, window);
+        if (!mbar_wait(bar + i % kStages, (i / kStages) & 1)) {
+            failed = true;
+            break;
+        }
+        const uint8_t *st = ring + (i % kStages) * R::kStage;
+        const int t0 = t_begin + kStep * (warp + kWarps4 * i);
+        const int page0 = __shfl_sync(0xffffffffu, pg, 2 * (i & 15)), page1 = __shfl_sync(0xffffffffu, pg, 2 * (i & 15) + 1);
+        // a step where some row does not see every token, or a page is not there
+        const bool edge = t0 + kStep > first_seen || t0 + kStep > t_end || page0 < 0 || page1 < 0;
+
+        // Scores.
+        float x[MT][4][4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[mt][u][e] = 0.f;
+            uint32_t code[D / 32], sc;
+            if constexpr (D == 128) {
+                const uint4 w = *reinterpret_cast<const uint4 *>(st + k_at + 4 * u * (D / 2));
+                code[0] = w.x; code[1] = w.y; code[2] = w.z; code[3] = w.w;
+                sc = scales2(*reinterpret_cast<const uint16_t *>(st + ks_at + 4 * u * (D / 16)));
+            } else {
+                const uint2 w = *reinterpret_cast<const uint2 *>(st + k_at + 4 * u * (D / 2));
+                code[0] = w.x; code[1] = w.y;
+                sc = scales2(st[ks_at + 4 * u * (D / 16)]);
+            }
+            const uint32_t s_lo = __byte_perm(sc, sc, 0x1010), s_hi = D == 128 ? __byte_perm(sc, sc, 0x3232) : s_lo;
+#pragma unroll
+            for (int w = 0; w < D / 32; ++w) {
+                uint32_t hh[4];
+                widen(code[w], hh);
+                const uint32_t s = w < D / 64 ? s_lo : s_hi;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const uint32_t b0 = mul2(hh[2 * e], s), b1 = mul2(hh[2 * e + 1], s);
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        const uint4 qa = sq[(mt * KS + 2 * w + e) * 32 + lane];
+                        const uint32_t av[4] = {qa.x, qa.y, qa.z, qa.w};
+                        mma16816(x[mt][u], av, b0, b1);
+                    }
+                }
+            }
+        }
+
+        // Softmax: running maximum and sum of this lane's two rows a tile.
+        const bool gone[2] = {page0 < 0, page1 < 0};
+        const bool mine_gone = gone[c >> 1];
+        uint32_t p[MT][2][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[mt][u][e] *= f[mt][e >> 1];
+            if (edge) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int t = t0 + 16 * (c >> 1) + 4 * u + 2 * (e & 1) + ((e & 1) ^ par);
+                        if (t >= seen[mt][e >> 1] || t >= t_end || mine_gone) x[mt][u][e] = -INFINITY;
+                    }
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) top[e >> 1] = fmaxf(top[e >> 1], x[mt][u][e]);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                top[k] = fmaxf(top[k], __shfl_xor_sync(0xffffffffu, top[k], 1));
+                top[k] = fmaxf(top[k], __shfl_xor_sync(0xffffffffu, top[k], 2));
+            }
+            if (__any_sync(0xffffffffu, top[0] > m[mt][0] + kLag || top[1] > m[mt][1] + kLag)) {
+                float fac[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float mn = fmaxf(m[mt][k], top[k]);
+                    fac[k] = mn == -INFINITY ? 1.f : ex2(m[mt][k] - mn);
+                    m[mt][k] = mn;
+                    l[mt][k] *= fac[k];
+                }
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[mt][j][e] *= fac[e >> 1];
+            }
+            // a row that has seen nothing yet keeps m = -inf and p = 2^-inf = 0
+            const float base[2] = {m[mt][0] == -INFINITY ? 0.f : m[mt][0], m[mt][1] == -INFINITY ? 0.f : m[mt][1]};
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                float e4[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    e4[e] = ex2(x[mt][u][e] - base[e >> 1]);
+                    l[mt][e >> 1] += e4[e];
+                }
+                p[mt][u >> 1][2 * (u & 1)] = f16x2(e4[0], e4[1]);
+                p[mt][u >> 1][2 * (u & 1) + 1] = f16x2(e4[2], e4[3]);
+            }
+        }
+
+        // Output.
+#pragma unroll
+        for (int ms = 0; ms < 2; ++ms) {
+            uint32_t code[2][2][D / 64], sc[2];  // [n-tile of the scores][token of the pair]
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt) {
+                uint32_t sb[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int idx = 8 * ms + 4 * nt + 2 * e + (e ^ par);
+                    if constexpr (D == 128) {
+                        const uint2 w = *reinterpret_cast<const uint2 *>(st + v_at + idx * (D / 2));
+                        code[nt][e][0] = w.x; code[nt][e][1] = w.y;
+                    } else {
+                        code[nt][e][0] = *reinterpret_cast<const uint32_t *>(st + v_at + idx * (D / 2));
+                    }
+                    sb[e] = st[vs_at + idx * (D / 16)];
+                    // what no row sees has weight 0 and may hold anything: its scale is set to 0
+                    if (edge && (mine_gone || t0 + 16 * (c >> 1) + idx >= t_end)) sb[e] = 0;
+                }
+                if (edge) {
+                    // A NaN here belongs to the rows that see its token and to no other: it leaves the
+                    // product and is put into their accumulators.
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        uint32_t bad = __ballot_sync(0xffffffffu, (sb[e] & 0x7f) == 0x7f);
+                        if (bad && (sb[e] & 0x7f) == 0x7f) sb[e] = 0;
+                        while (bad) {
+                            const int src = __ffs(bad) - 1, col = src >> 2, sc_c = src & 3;
+                            bad &= bad - 1;
+                            const int t = t0 + 16 * (sc_c >> 1) + 8 * ms + 4 * nt + 2 * e + (e ^ (sc_c & 1));
+                            if (c != col >> 1) continue;
+#pragma unroll
+                            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                                for (int k = 0; k < 2; ++k)
+                                    if (t < seen[mt][k])
+#pragma unroll
+                                        for (int j = 0; j < NT; ++j) {
+                                            if (col & 1) o[mt][j][2 * k + 1] = NAN;
+                                            else o[mt][j][2 * k] = NAN;
+                                        }
+                        }
+                        __syncwarp();
+                    }
+                }
+                sc[nt] = scales2(sb[0] | sb[1] << 8);
+            }
+#pragma unroll
+            for (int w = 0; w < D / 64; ++w) {
+                uint32_t ev[2][4], od[2][4];  // channels 8 w + {0, 2, 4, 6} and + {1, 3, 5, 7}, as token pairs
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt) {
+                    const uint32_t w0 = code[nt][0][w], w1 = code[nt][1][w];
+                    widen((w0 & 0x0f0f0f0fu) | ((w1 << 4) & 0xf0f0f0f0u), ev[nt]);
+                    widen(((w0 >> 4) & 0x0f0f0f0fu) | (w1 & 0xf0f0f0f0u), od[nt]);
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t e0 = mul2(ev[0][k], sc[0]), e1 = mul2(ev[1][k], sc[1]);
+                    const uint32_t d0 = mul2(od[0][k], sc[0]), d1 = mul2(od[1][k], sc[1]);
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        mma16816(o[mt][8 * w + 2 * k], p[mt][ms], e0, e1);
+                        mma16816(o[mt][8 * w + 2 * k + 1], p[mt][ms], d0, d1);
+                    }
+                }
+            }
+        }
+        __syncwarp();  // the stage is free
+    }
+    if (failed) {  // wait for what is still in flight, within the same bound
+        if (lane == 0) report_opt(a.err, DEV_PIPE_TIMEOUT, b, h, t_begin);
+        for (int s = 0; s < kStages; ++s) mbar_wait(bar + s, 0), mbar_wait(bar + s, 1);
     }
 #pragma unroll
-    for (int e = 0; e < E; ++e) a.out[at + e] = __float2bfloat16_rn(ll > 0.f || ll != ll ? o[e] / ll : 0.f);
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            l[mt][k] += __shfl_xor_sync(0xffffffffu, l[mt][k], 1);
+            l[mt][k] += __shfl_xor_sync(0xffffffffu, l[mt][k], 2);
+            if (c == 0) sml[(warp * MT + mt) * 16 + g + 8 * k] = make_float2(m[mt][k], l[mt][k]);
+        }
+    if (__syncthreads_or(failed)) return;
+
+    // Join the warps: each scales its rows to the common maximum, then the sums are added from shared memory.
+    float *so = reinterpret_cast<float *>(sm);
+    constexpr int kRow = D + 4;
+    const int64_t unit = (((int64_t)b * a.kv.Hk + h) * a.tiles + tile) * a.splits + split;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        if (mt) __syncthreads();
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            float top = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kWarps4; ++w) top = fmaxf(top, sml[(w * MT + mt) * 16 + g + 8 * k].x);
+            const float fac = m[mt][k] == -INFINITY ? 1.f : ex2(m[mt][k] - top);
+            float *dst = so + (warp * 16 + g + 8 * k) * kRow;
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int j = 0; j < NT; j += 4)
+                    *reinterpret_cast<float4 *>(dst + (2 * c + e) * (D / 8) + j) =
+                        make_float4(o[mt][j][2 * k + e] * fac, o[mt][j + 1][2 * k + e] * fac,
+                                    o[mt][j + 2][2 * k + e] * fac, o[mt][j + 3][2 * k + e] * fac);
+        }
+        __syncthreads();
+        // 8 threads a row, D / 8 channels each
+        const int row = tid >> 3, at = (tid & 7) * (D / 8);
+        float top = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps4; ++w) top = fmaxf(top, sml[(w * MT + mt) * 16 + row].x);
+#pragma unroll
+        for (int w = 0; w < kWarps4; ++w) {
+            const float2 ml = sml[(w * MT + mt) * 16 + row];
+            sum += ml.x == -INFINITY ? ml.y : ml.y * ex2(ml.x - top);
+        }
+        float acc[D / 8];
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j) {
+            acc[j] = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps4; ++w) acc[j] += so[(w * 16 + row) * kRow + at + j];
+        }
+        const int grow = row0 + 16 * mt + row;
+        if (grow >= rows) continue;
+        if (ns == 1) {
+            const float inv = sum == 0.f ? 0.f : a.kv.v_scale / sum;
+            const int i = grow / G, hd = grow - i * G;
+            uint32_t w[D / 16];
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) {
+                const __nv_bfloat162 v = __floats2bfloat162_rn(acc[2 * j] * inv, acc[2 * j + 1] * inv);
+                w[j] = *reinterpret_cast<const uint32_t *>(&v);
+            }
+            uint4 *dst = reinterpret_cast<uint4 *>(a.out + ((int64_t)(r0 + i) * a.Hq + h * G + hd) * D + at);
+#pragma unroll
+            for (int j = 0; j < D / 64; ++j) dst[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+        } else {
+            float4 *dst = reinterpret_cast<float4 *>(a.part + (unit * RT + 16 * mt + row) * D + at);
+#pragma unroll
+            for (int j = 0; j < D / 32; ++j) dst[j] = make_float4(acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]);
+            if ((tid & 7) == 0) {
+                float2 *ml = reinterpret_cast<float2 *>(a.part + (int64_t)a.B * a.kv.Hk * a.tiles * a.splits * RT * D);
+                ml[unit * RT + 16 * mt + row] = make_float2(top, sum);
+            }
+        }
+    }
 }
 
-bool attend_valid(const rssm_kv4_config *c, const rssm_attend_config *t, Kv4Args *kv) {
+// Join the splits of one tile: out = sum_s 2^{m_s - m} O_s / sum_s 2^{m_s - m} l_s.
+template <int D, int MT>
+__global__ void __launch_bounds__(256) attend_join_kernel(const AttendArgs a) {
+    constexpr int RT = 16 * MT, TPR = D / 4;  // threads a row, 4 channels each
+    const int tile = blockIdx.x % a.tiles, h = blockIdx.x / a.tiles, b = blockIdx.y;
+    int r0, n, len;
+    if (!attend_request(a, b, r0, n, len)) return;  // reported by the first kernel
+    const int rows = n * a.G, row0 = tile * RT;
+    if (row0 >= rows) return;
+    const int last = min(row0 + RT, rows) - 1;
+    const int ns = (max(0, len - n + last / a.G + 1) + a.L - 1) / a.L;
+    if (ns <= 1) return;
+    const int64_t unit = (((int64_t)b * a.kv.Hk + h) * a.tiles + tile) * a.splits;
+    const float2 *ml = reinterpret_cast<const float2 *>(a.part + (int64_t)a.B * a.kv.Hk * a.tiles * a.splits * RT * D);
+    for (int r = threadIdx.x / TPR; r < min(RT, rows - row0); r += 256 / TPR) {
+        const int at = (threadIdx.x % TPR) * 4;
+        float top = -INFINITY, sum = 0.f;
+        for (int s = 0; s < ns; ++s) top = fmaxf(top, ml[(unit + s) * RT + r].x);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int s = 0; s < ns; ++s) {
+            const float2 v = ml[(unit + s) * RT + r];
+            const float fac = v.x == -INFINITY ? 1.f : ex2(v.x - top);
+            const float4 x = *reinterpret_cast<const float4 *>(a.part + ((unit + s) * RT + r) * D + at);
+            sum += v.y * fac;
+            acc.x += x.x * fac; acc.y += x.y * fac; acc.z += x.z * fac; acc.w += x.w * fac;
+        }
+        const float inv = sum == 0.f ? 0.f : a.kv.v_scale / sum;
+        const int i = (row0 + r) / a.G, hd = row0 + r - i * a.G;
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+        *reinterpret_cast<uint2 *>(a.out + ((int64_t)(r0 + i) * a.Hq + h * a.G + hd) * D + at) =
+            make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+    }
+}
+
+float score_scale(float sm_scale, float k_scale) { return sm_scale * k_scale * 1.4426950408889634f; }
+
+// Sizes of the launch.  Row tiles of 32 where a request can have more than 16 rows.
+struct Plan {
+    int mt, tiles, splits, L;
+    size_t bytes;
+};
+
+bool attend_plan(const rssm_kv4_config *c, const rssm_attend_config *t, Kv4Args *kv, Plan *p) {
     if (!kv4_args(c, kv) || !t) return false;
     if (t->batch < 1 || t->batch > 65535 || t->n_q_heads < 1 || t->n_q_heads > 65535 || t->n_q_heads % kv->Hk != 0)
         return false;
-    if (t->tokens < 1 || t->max_pages < 1 || t->max_q < 1 || t->max_seq < 1 || !isfinite(t->sm_scale)) return false;
+    if (t->tokens < 1 || t->max_pages < 1 || t->max_q < 1 || t->max_seq < 1) return false;
+    if (!isfinite(score_scale(t->sm_scale, kv->k_scale))) return false;
+    const int64_t max_q = t->max_q < t->tokens ? t->max_q : t->tokens;
+    const int64_t rows = max_q * (t->n_q_heads / kv->Hk);
+    if (rows > 0x3fffffff) return false;
+    p->mt = rows > 16 ? 2 : 1;
+    const int64_t tiles = (rows + 16 * p->mt - 1) / (16 * p->mt);
+    if (tiles * kv->Hk > 65535) return false;
+    int64_t seq = (int64_t)t->max_pages * kv->ps;
+    if (t->max_seq < seq) seq = t->max_seq;
+    // Split the context where the tiles alone do not fill the machine (148 SMs, 3 CTAs each) twice over.
+    const int64_t units = (int64_t)t->batch * kv->Hk * tiles, want = 148 * 3 * 2;
+    int64_t splits = (want + units - 1) / units, most = (seq + 255) / 256;
+    if (splits > most) splits = most;
+    if (splits < 1) splits = 1;
+    const int64_t L = ((seq + splits - 1) / splits + 127) / 128 * 128;
+    splits = (seq + L - 1) / L;
+    p->tiles = (int)tiles;
+    p->splits = (int)splits;
+    p->L = (int)L;
+    p->bytes = splits > 1 ? (size_t)(units * splits * 16 * p->mt) * (size_t)(kv->D + 2) * 4 : 0;
     return true;
+}
+
+template <int D, int MT>
+cudaError_t attend_launch(const AttendArgs &a, cudaStream_t st) {
+    cudaError_t e = cudaFuncSetAttribute(attend_kernel<D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D, MT>::kBytes);
+    if (e != cudaSuccess) return e;
+    attend_kernel<D, MT><<<dim3(a.splits, a.tiles * a.kv.Hk, a.B), 32 * kWarps4, Smem<D, MT>::kBytes, st>>>(a);
+    if ((e = cudaGetLastError()) != cudaSuccess || a.splits == 1) return e;
+    attend_join_kernel<D, MT><<<dim3(a.tiles * a.kv.Hk, a.B), 256, 0, st>>>(a);
+    return cudaGetLastError();
 }
 
 }  // namespace
@@ -124,7 +622,9 @@ bool attend_valid(const rssm_kv4_config *c, const rssm_attend_config *t, Kv4Args
 extern "C" {
 
 RSSM_API size_t rssm_kv4_attend_workspace_bytes(const rssm_kv4_config *cfg, const rssm_attend_config *att) {
-    return 0;
+    rssm::Kv4Args kv;
+    rssm::Plan p;
+    return rssm::attend_plan(cfg, att, &kv, &p) ? p.bytes : 0;
 }
 
 RSSM_API rssm_status rssm_kv4_attend(const rssm_kv4_config *cfg, const rssm_attend_config *att, const void *q,
@@ -133,15 +633,22 @@ RSSM_API rssm_status rssm_kv4_attend(const rssm_kv4_config *cfg, const rssm_atte
                                      int32_t *dev_error, void *stream) {
     using namespace rssm;
     AttendArgs a{};
-    if (!attend_valid(cfg, att, &a.kv) || !q || !cache || !block_table || !seq_len || !cu_q || !out) return RSSM_EINVAL;
+    Plan p;
+    if (!attend_plan(cfg, att, &a.kv, &p) || !q || !cache || !block_table || !seq_len || !cu_q || !out)
+        return RSSM_EINVAL;
     if (!aligned16(q) || !aligned16(cache) || !aligned16(out)) return RSSM_EINVAL;
-    a.B = att->batch; a.Hq = att->n_q_heads; a.tokens = att->tokens; a.max_pages = att->max_pages;
-    a.max_q = att->max_q; a.max_seq = att->max_seq; a.scale = att->sm_scale;
+    if (p.bytes && (!workspace || workspace_bytes < p.bytes || ((uintptr_t)workspace & 255))) return RSSM_EINVAL;
+    a.B = att->batch; a.Hq = att->n_q_heads; a.G = att->n_q_heads / a.kv.Hk; a.tokens = att->tokens;
+    a.max_pages = att->max_pages; a.max_q = att->max_q; a.max_seq = att->max_seq;
+    a.tiles = p.tiles; a.splits = p.splits; a.L = p.L;
+    a.scale = score_scale(att->sm_scale, a.kv.k_scale);
     a.q = (const __nv_bfloat16 *)q; a.cache = (const uint8_t *)cache;
-    a.table = block_table; a.seq_len = seq_len; a.cu = cu_q; a.out = (__nv_bfloat16 *)out; a.err = dev_error;
-    auto k = a.kv.D == 64 ? attend_rows_kernel<64> : attend_rows_kernel<128>;
-    k<<<dim3(a.max_q, a.Hq, a.B), 32 * kAttWarps, 0, (cudaStream_t)stream>>>(a);
-    return cudaGetLastError() == cudaSuccess ? RSSM_OK : RSSM_ECUDA;
+    a.table = block_table; a.seq_len = seq_len; a.cu = cu_q; a.out = (__nv_bfloat16 *)out; a.part = (float *)workspace;
+    a.err = dev_error;
+    const cudaStream_t st = (cudaStream_t)stream;
+    const cudaError_t e = a.kv.D == 64 ? (p.mt == 1 ? attend_launch<64, 1>(a, st) : attend_launch<64, 2>(a, st))
+                                       : (p.mt == 1 ? attend_launch<128, 1>(a, st) : attend_launch<128, 2>(a, st));
+    return e == cudaSuccess ? RSSM_OK : RSSM_ECUDA;
 }
 
 }  // extern "C"
