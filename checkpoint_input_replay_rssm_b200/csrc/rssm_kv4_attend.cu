@@ -22,8 +22,8 @@
 // 2^6, so that the accumulators are rescaled a few times per row and not each step.
 //
 // A warp streams its own tokens: 32 at a time, every kWarps-th group of 32 of the
-// CTA's range, by bulk copies into a ring of kStages stages of its own; the warps of a CTA meet
-// only at the end, to join their sums.  Long contexts are split over CTAs and
+// CTA's range, by asynchronous copies into a ring of kStages stages of its own; the warps of a
+// CTA meet only at the end, to join their sums.  Long contexts are split over CTAs and
 // joined by a second kernel.
 #include <cuda_bf16.h>
 
@@ -31,7 +31,6 @@
 
 #include "rssm_internal.h"
 #include "rssm_kv4.cuh"
-#include "rssm_pipe.cuh"
 
 namespace rssm {
 
@@ -51,7 +50,7 @@ struct AttendArgs {
 };
 
 constexpr int kWarps4 = 4;
-constexpr int kStages = 4;
+constexpr int kStages = 3;
 constexpr int kStep = 32;        // tokens a warp takes at a time
 constexpr float kLag = 6.f;      // log2 by which the running maximum may trail
 
@@ -67,8 +66,8 @@ template <int D, int MT> struct Smem {
     static constexpr int kMerge = kWarps4 * 16 * (D + 4) * 4;  // over the ring, one 16-row tile at a time
     static constexpr int kQ = kRing > kMerge ? kRing : kMerge;
     static constexpr int kMl = kQ + MT * (D / 16) * 512;       // query operands: [mt][k-step][lane] 16 bytes
-    static constexpr int kBar = kMl + kWarps4 * MT * 16 * 8;   // (m, l) of every warp and row
-    static constexpr int kBytes = kBar + kWarps4 * kStages * 8;
+    static constexpr int kRow = kMl + kWarps4 * MT * 16 * 8;   // (m, l) of every warp and row
+    static constexpr int kBytes = kRow + MT * 16 * 8;          // score factor and visible tokens of every row
 };
 
 // The rows and length of request b; false (and reported) where they do not fit the call.
@@ -109,19 +108,26 @@ __device__ __forceinline__ uint32_t scales2(uint32_t w) {
     return r;
 }
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+__device__ __forceinline__ void cp_async16_or_zero(void *dst, const void *src, bool live) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
+                 "r"(live ? 16 : 0)
+                 : "memory");
+}
+
 // A row's power-of-two scale: the largest magnitude goes to [2^9, 2^10).
 __device__ __forceinline__ int row_exponent(float top) {
-    if (!(top > 0.f) || top > 3.4e38f) return 0;
-    int e;
-    frexpf(top, &e);
-    return e - 10;
+    const int e = (int)(__float_as_uint(top) >> 23);  // top >= 0
+    return e == 0 || e == 255 ? 0 : e - 126 - 10;
 }
+
+// 2^e for e in -126 .. 127.
+__device__ __forceinline__ float pow2f(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
 template <int D, int MT>
 __global__ void __launch_bounds__(32 * kWarps4, MT == 1 ? 3 : 2) attend_kernel(const AttendArgs a) {
@@ -152,104 +158,120 @@ __global__ void __launch_bounds__(32 * kWarps4, MT == 1 ? 3 : 2) attend_kernel(c
     uint8_t *ring = sm + warp * kStages * R::kStage;
     uint4 *sq = reinterpret_cast<uint4 *>(sm + S::kQ);
     float2 *sml = reinterpret_cast<float2 *>(sm + S::kMl);
-    uint64_t *bar = reinterpret_cast<uint64_t *>(sm + S::kBar) + warp * kStages;
-    if (lane == 0) {
-#pragma unroll
-        for (int s = 0; s < kStages; ++s) mbar_init(bar + s, 1);
-        mbar_init_fence();
-    }
-    __syncwarp();
+    float *sf = reinterpret_cast<float *>(sm + S::kRow);
+    int *sseen = reinterpret_cast<int *>(sm + S::kRow) + RT;
 
     // This warp's steps: tokens t_begin + 32 (warp + kWarps4 i).  Lane l keeps the page of
     // 16-token group l & 1 of step l >> 1 of a window of 16 steps, -1 for one that is not
     // read (behind the last token, or outside the cache).
     const int steps_all = (max(0, t_end - t_begin) + kStep - 1) / kStep;
     const int steps = steps_all > warp ? (steps_all - warp + kWarps4 - 1) / kWarps4 : 0;
+    // The group's place in its page goes with it: 16 page + place (ps <= 256).
     auto pages_of = [&](int win) {
         const int i = win * 16 + (lane >> 1);
         const int t = t_begin + kStep * (warp + kWarps4 * i) + 16 * (lane & 1);
         int page = -1;
         if (i < steps && t < t_end) {
-            page = a.table[(int64_t)b * a.max_pages + t / ps];
+            const int at = t / ps;
+            page = a.table[(int64_t)b * a.max_pages + at];
             if (page < 0 || page >= a.kv.pages) {
                 report_opt(a.err, DEV_BAD_PAGE, b, h, page);
                 page = -1;
+            } else {
+                page = page * 16 + ((t - at * ps) >> 4);
             }
         }
         return page;
     };
     int pg = pages_of(0), pg_next = pages_of(1);
     const int64_t head_bytes = kv4_head_bytes(ps, D);
-    // Start the copies of step i: lane 4 gr + piece copies that piece of 16-token group gr.
-    auto issue = [&](int i, int window) {
-        const int gr = (lane >> 2) & 1, piece = lane & 3;
-        const int pw = (i >> 4) == window ? pg : pg_next;
-        const int page = __shfl_sync(0xffffffffu, pw, 2 * (i & 15) + gr);
-        const int other = __shfl_xor_sync(0xffffffffu, page, 4);
-        uint64_t *br = bar + i % kStages;
-        if (lane == 0) mbar_arrive_expect_tx(br, R::kGran * ((page >= 0) + (other >= 0)));
-        __syncwarp();
-        if (lane < 8 && page >= 0 && (piece == 0 || ps != 16)) {
-            const int off = (t_begin + kStep * (warp + kWarps4 * i) + 16 * gr) % ps;
-            const uint8_t *src = a.cache + ((int64_t)page * a.kv.Hk + h) * head_bytes;
-            uint8_t *dst = ring + (i % kStages) * R::kStage + gr * (R::kGran + R::kPad);
-            if (ps == 16) {  // a page is laid out as a group is
-                bulk_g2s(dst, src, R::kGran, br);
-            } else {
-                const bool sc = piece & 1, v = piece & 2;
-                src += (v ? ps * (D * 9 / 16) : 0) + (sc ? ps * (D / 2) + off * (D / 16) : off * (D / 2));
-                bulk_g2s(dst + (v ? R::kV : 0) + (sc ? R::kScale : 0), src, sc ? D : R::kScale, br);
+    // Start the copies of step i into stage sg, 16 bytes a lane at a time: the codes of a group are D / 64
+    // such rounds for keys and as many for values, the scales of both groups are one round.  A group that
+    // is not read is filled with zeros.
+    const int64_t page_bytes = a.kv.Hk * head_bytes;
+    const int v_src = ps * (D * 9 / 16);  // values behind keys in a page
+    const int sc_gr = lane / (D / 8), sc_v = (lane / (D / 16)) & 1, sc_at = (lane % (D / 16)) * 16;
+    const int sc_src = sc_v * v_src + ps * (D / 2) + sc_at;
+    uint8_t *sc_dst = ring + (sc_gr & 1) * (R::kGran + R::kPad) + sc_v * R::kV + R::kScale + sc_at;
+    auto issue = [&](int i, int sg, int window) {
+        const int gp = (i >> 4) == window ? pg : pg_next;
+        const uint8_t *sc_from = a.cache;
+        int sc_live = 0;
+#pragma unroll
+        for (int gr = 0; gr < 2; ++gr) {
+            const int at = __shfl_sync(0xffffffffu, gp, 2 * (i & 15) + gr);
+            const bool live = at >= 0;
+            const int page = live ? at >> 4 : 0, place = live ? at & 15 : 0;
+            const uint8_t *src = a.cache + page * page_bytes + h * head_bytes;
+            uint8_t *dst = ring + sg * R::kStage + gr * (R::kGran + R::kPad) + lane * 16;
+#pragma unroll
+            for (int k = 0; k < D / 64; ++k) {
+                cp_async16_or_zero(dst + 512 * k, src + place * R::kScale + lane * 16 + 512 * k, live);
+                cp_async16_or_zero(dst + R::kV + 512 * k, src + v_src + place * R::kScale + lane * 16 + 512 * k, live);
+            }
+            if (sc_gr == gr) {
+                sc_from = src + place * D + sc_src;
+                sc_live = live;
             }
         }
+        if (sc_gr < 2) cp_async16_or_zero(sc_dst + sg * R::kStage, sc_from, sc_live);
     };
-    for (int i = 0; i < kStages - 1 && i < steps; ++i) issue(i, 0);
+#pragma unroll 1
+    for (int i = 0; i < kStages - 1; ++i) {
+        if (i < steps) issue(i, i, 0);
+        cp_async_commit();
+    }
 
-    // Query operands of the tile's rows, made by the warps in turn: [mt][k-step][lane].
+    // Query operands, [mt][k-step][lane]: warp w makes those of the rows g + 8 (w & 1) of 16-row tile w >> 1.
+    if (warp < 2 * MT) {
+        const int mt = warp >> 1, u = warp & 1, row = row0 + 16 * mt + g + 8 * u;
+        const bool live = row < rows;
+        const int i = live ? row / G : 0, hd = live ? row - i * G : 0;
+        const uint4 *src =
+            reinterpret_cast<const uint4 *>(a.q + ((int64_t)(r0 + i) * a.Hq + h * G + hd) * D + c * (D / 4));
+        uint4 raw[D / 32];
+        float top = 0.f;
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) {
+            raw[k] = live ? src[k] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t x = (&raw[k].x)[e];
+                top = fmaxf(top, fmaxf(fabsf(bf16_bits_to_float(x & 0xffff)), fabsf(bf16_bits_to_float(x >> 16))));
+            }
+        }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const int ex = row_exponent(top);
+        // 2^-ex as two factors: one alone may leave fp32's range.  The score's factor is
+        // kept above 0 (its sign goes to the query, a zero scale becomes a zero query), so
+        // that the largest raw score is the largest score and a masked one stays -inf.
+        const float s0 = copysignf(pow2f(-(ex / 2)), a.scale);
+        const float s1 = a.scale == 0.f ? 0.f : pow2f(-(ex - ex / 2));
+        if (c == 0) {
+            sf[16 * mt + g + 8 * u] = fmaxf(fabsf(a.scale) * pow2f(ex / 2) * pow2f(ex - ex / 2), 1.2e-38f);
+            sseen[16 * mt + g + 8 * u] = live ? len - n + i + 1 : 0;
+        }
+        uint32_t *dst = reinterpret_cast<uint32_t *>(sq) + (mt * KS * 32 + lane) * 4 + u;
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t x = (&raw[k].x)[e];
+                dst[(2 * k + (e >> 1)) * 128 + 2 * (e & 1)] =
+                    f16x2(bf16_bits_to_float(x & 0xffff) * s0 * s1, bf16_bits_to_float(x >> 16) * s0 * s1);
+            }
+    }
+    __syncthreads();
     float f[MT][2];   // factor of this lane's rows' scores
     int seen[MT][2];  // tokens that they see
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-        uint32_t w[2][KS][2];  // [row][k-step][channels 0-1, 2-3 of the step's four]
+    for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            const int row = row0 + 16 * mt + g + 8 * u;
-            const bool live = row < rows;
-            const int i = live ? row / G : 0, hd = live ? row - i * G : 0;
-            seen[mt][u] = live ? len - n + i + 1 : 0;
-            const uint4 *src = reinterpret_cast<const uint4 *>(
-                a.q + ((int64_t)(r0 + i) * a.Hq + h * G + hd) * D + c * (D / 4));
-            uint4 raw[D / 32];
-            float top = 0.f;
-#pragma unroll
-            for (int k = 0; k < D / 32; ++k) {
-                raw[k] = live ? src[k] : make_uint4(0, 0, 0, 0);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint32_t x = (&raw[k].x)[e];
-                    top = fmaxf(top, fmaxf(fabsf(bf16_bits_to_float(x & 0xffff)), fabsf(bf16_bits_to_float(x >> 16))));
-                }
-            }
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const int ex = row_exponent(top);
-            // 2^-ex as two factors: one alone may leave fp32's range
-            const float s0 = ldexpf(1.f, -(ex / 2)), s1 = ldexpf(1.f, -(ex - ex / 2));
-            f[mt][u] = ldexpf(a.scale, ex);
-#pragma unroll
-            for (int k = 0; k < D / 32; ++k)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint32_t x = (&raw[k].x)[e];
-                    w[u][2 * k + (e >> 1)][e & 1] = f16x2(bf16_bits_to_float(x & 0xffff) * s0 * s1,
-                                                          bf16_bits_to_float(x >> 16) * s0 * s1);
-                }
+            f[mt][u] = sf[16 * mt + g + 8 * u];
+            seen[mt][u] = sseen[16 * mt + g + 8 * u];
         }
-        if (warp == mt % kWarps4)
-#pragma unroll
-            for (int s = 0; s < KS; ++s)
-                sq[(mt * KS + s) * 32 + lane] = make_uint4(w[0][s][0], w[1][s][0], w[0][s][1], w[1][s][1]);
-    }
-    __syncthreads();
 
     float o[MT][NT][4], m[MT][2], l[MT][2];
 #pragma unroll
@@ -271,59 +293,63 @@ __global__ void __launch_bounds__(32 * kWarps4, MT == 1 ? 3 : 2) attend_kernel(c
     const int vs_at = (c >> 1) * (R::kGran + R::kPad) + R::kV + R::kScale + (D == 128 ? g : g >> 1);
     const int par = c & 1;
 
-    bool failed = false;
+    uint32_t nan_cols = 0;  // bit 2 (2 mt + k) + e: row g + 8 k saw a NaN value in block 2 c + e
+    int sg = 0;
     for (int i = 0; i < steps; ++i) {
         const int window = i >> 4;
         if ((i & 15) == 0 && i > 0) {
             pg = pg_next;
             pg_next = pages_of(window + 1);
         }
-        if (i + kStages - 1 < steps) issue(i + kStages - 1, window);
-        if (!mbar_wait(bar + i % kStages, (i / kStages) & 1)) {
-            failed = true;
-            break;
-        }
-        const uint8_t *st = ring + (i % kStages) * R::kStage;
+        if (i + kStages - 1 < steps) issue(i + kStages - 1, sg == 0 ? kStages - 1 : sg - 1, window);
+        cp_async_commit();
+        cp_async_wait_group<kStages - 1>();
+        __syncwarp();  // the other lanes' copies are there too
+        const uint8_t *st = ring + sg * R::kStage;
+        if (++sg == kStages) sg = 0;
         const int t0 = t_begin + kStep * (warp + kWarps4 * i);
         const int page0 = __shfl_sync(0xffffffffu, pg, 2 * (i & 15)), page1 = __shfl_sync(0xffffffffu, pg, 2 * (i & 15) + 1);
         // a step where some row does not see every token, or a page is not there
         const bool edge = t0 + kStep > first_seen || t0 + kStep > t_end || page0 < 0 || page1 < 0;
 
-        // Scores.
+        // Scores: the four n-tiles side by side, so that their chains of k-steps overlap.
         float x[MT][4][4];
+        uint32_t code[4][D / 32], ksc[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) x[mt][u][e] = 0.f;
-            uint32_t code[D / 32], sc;
             if constexpr (D == 128) {
                 const uint4 w = *reinterpret_cast<const uint4 *>(st + k_at + 4 * u * (D / 2));
-                code[0] = w.x; code[1] = w.y; code[2] = w.z; code[3] = w.w;
-                sc = scales2(*reinterpret_cast<const uint16_t *>(st + ks_at + 4 * u * (D / 16)));
+                code[u][0] = w.x; code[u][1] = w.y; code[u][2] = w.z; code[u][3] = w.w;
+                ksc[u] = scales2(*reinterpret_cast<const uint16_t *>(st + ks_at + 4 * u * (D / 16)));
             } else {
                 const uint2 w = *reinterpret_cast<const uint2 *>(st + k_at + 4 * u * (D / 2));
-                code[0] = w.x; code[1] = w.y;
-                sc = scales2(st[ks_at + 4 * u * (D / 16)]);
+                code[u][0] = w.x; code[u][1] = w.y;
+                ksc[u] = scales2(st[ks_at + 4 * u * (D / 16)]);
             }
-            const uint32_t s_lo = __byte_perm(sc, sc, 0x1010), s_hi = D == 128 ? __byte_perm(sc, sc, 0x3232) : s_lo;
+        }
 #pragma unroll
-            for (int w = 0; w < D / 32; ++w) {
-                uint32_t hh[4];
-                widen(code[w], hh);
-                const uint32_t s = w < D / 64 ? s_lo : s_hi;
+        for (int w = 0; w < D / 32; ++w) {
+            uint32_t hh[4][4];
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const uint32_t b0 = mul2(hh[2 * e], s), b1 = mul2(hh[2 * e + 1], s);
+            for (int u = 0; u < 4; ++u) {
+                const uint32_t sc = __byte_perm(ksc[u], ksc[u], w < D / 64 ? 0x1010 : D == 128 ? 0x3232 : 0x1010);
+                widen(code[u][w], hh[u]);
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        const uint4 qa = sq[(mt * KS + 2 * w + e) * 32 + lane];
-                        const uint32_t av[4] = {qa.x, qa.y, qa.z, qa.w};
-                        mma16816(x[mt][u], av, b0, b1);
-                    }
+                for (int e = 0; e < 4; ++e) hh[u][e] = mul2(hh[u][e], sc);
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    const uint4 qa = sq[(mt * KS + 2 * w + e) * 32 + lane];
+                    const uint32_t av[4] = {qa.x, qa.y, qa.z, qa.w};
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) mma16816(x[mt][u], av, hh[u][2 * e], hh[u][2 * e + 1]);
                 }
-            }
         }
 
         // Softmax: running maximum and sum of this lane's two rows a tile.
@@ -333,18 +359,14 @@ __global__ void __launch_bounds__(32 * kWarps4, MT == 1 ? 3 : 2) attend_kernel(c
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             float top[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x[mt][u][e] *= f[mt][e >> 1];
             if (edge) {
+                const int lim[2] = {mine_gone ? 0 : min(seen[mt][0], t_end) - t0 - 16 * (c >> 1),
+                                    mine_gone ? 0 : min(seen[mt][1], t_end) - t0 - 16 * (c >> 1)};
 #pragma unroll
                 for (int u = 0; u < 4; ++u)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int t = t0 + 16 * (c >> 1) + 4 * u + 2 * (e & 1) + ((e & 1) ^ par);
-                        if (t >= seen[mt][e >> 1] || t >= t_end || mine_gone) x[mt][u][e] = -INFINITY;
-                    }
+                    for (int e = 0; e < 4; ++e)
+                        if (4 * u + 2 * (e & 1) + ((e & 1) ^ par) >= lim[e >> 1]) x[mt][u][e] = -INFINITY;
             }
 #pragma unroll
             for (int u = 0; u < 4; ++u)
@@ -353,7 +375,7 @@ __global__ void __launch_bounds__(32 * kWarps4, MT == 1 ? 3 : 2) attend_kernel(c
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 top[k] = fmaxf(top[k], __shfl_xor_sync(0xffffffffu, top[k], 1));
-                top[k] = fmaxf(top[k], __shfl_xor_sync(0xffffffffu, top[k], 2));
+                top[k] = fmaxf(top[k], __shfl_xor_sync(0xffffffffu, top[k], 2)) * f[mt][k];
             }
             if (__any_sync(0xffffffffu, top[0] > m[mt][0] + kLag || top[1] > m[mt][1] + kLag)) {
                 float fac[2];
@@ -376,7 +398,7 @@ __global__ void __launch_bounds__(32 * kWarps4, MT == 1 ? 3 : 2) attend_kernel(c
                 float e4[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    e4[e] = ex2(x[mt][u][e] - base[e >> 1]);
+                    e4[e] = ex2(fmaf(x[mt][u][e], f[mt][e >> 1], -base[e >> 1]));
                     l[mt][e >> 1] += e4[e];
                 }
                 p[mt][u >> 1][2 * (u & 1)] = f16x2(e4[0], e4[1]);
@@ -385,12 +407,34 @@ __global__ void __launch_bounds__(32 * kWarps4, MT == 1 ? 3 : 2) attend_kernel(c
         }
 
         // Output.
+        uint32_t vsc[8];  // this lane's scales: [16-token step][n-tile of the scores][token of the pair]
+#pragma unroll
+        for (int k = 0; k < 8; ++k) vsc[k] = st[vs_at + (4 * (k >> 1) + 2 * (k & 1) + ((k & 1) ^ par)) * (D / 16)];
+        if (edge) {
+            // What no row sees has weight 0 and may hold anything: its scale is set to 0.  A NaN belongs to
+            // the rows that see its token and to no other (0 NaN is NaN): it leaves the product, and the
+            // rows that see it are marked.
+            const int lim = mine_gone ? 0 : t_end - t0 - 16 * (c >> 1);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int idx = 4 * (k >> 1) + 2 * (k & 1) + ((k & 1) ^ par);
+                if (idx >= lim) vsc[k] = 0;
+                uint32_t bad = __ballot_sync(0xffffffffu, (vsc[k] & 0x7f) == 0x7f);
+                if ((vsc[k] & 0x7f) == 0x7f) vsc[k] = 0;
+                for (; bad; bad &= bad - 1) {
+                    const int col = (__ffs(bad) - 1) >> 2, cc = (__ffs(bad) - 1) & 3;
+                    const int t = t0 + 16 * (cc >> 1) + 4 * (k >> 1) + 2 * (k & 1) + ((k & 1) ^ (cc & 1));
+#pragma unroll
+                    for (int r = 0; r < 2 * MT; ++r)
+                        if (c == col >> 1 && t < seen[r >> 1][r & 1]) nan_cols |= 1u << (2 * r + (col & 1));
+                }
+            }
+        }
 #pragma unroll
         for (int ms = 0; ms < 2; ++ms) {
             uint32_t code[2][2][D / 64], sc[2];  // [n-tile of the scores][token of the pair]
 #pragma unroll
             for (int nt = 0; nt < 2; ++nt) {
-                uint32_t sb[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int idx = 8 * ms + 4 * nt + 2 * e + (e ^ par);
@@ -400,37 +444,8 @@ __global__ void __launch_bounds__(32 * kWarps4, MT == 1 ? 3 : 2) attend_kernel(c
                     } else {
                         code[nt][e][0] = *reinterpret_cast<const uint32_t *>(st + v_at + idx * (D / 2));
                     }
-                    sb[e] = st[vs_at + idx * (D / 16)];
-                    // what no row sees has weight 0 and may hold anything: its scale is set to 0
-                    if (edge && (mine_gone || t0 + 16 * (c >> 1) + idx >= t_end)) sb[e] = 0;
                 }
-                if (edge) {
-                    // A NaN here belongs to the rows that see its token and to no other: it leaves the
-                    // product and is put into their accumulators.
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        uint32_t bad = __ballot_sync(0xffffffffu, (sb[e] & 0x7f) == 0x7f);
-                        if (bad && (sb[e] & 0x7f) == 0x7f) sb[e] = 0;
-                        while (bad) {
-                            const int src = __ffs(bad) - 1, col = src >> 2, sc_c = src & 3;
-                            bad &= bad - 1;
-                            const int t = t0 + 16 * (sc_c >> 1) + 8 * ms + 4 * nt + 2 * e + (e ^ (sc_c & 1));
-                            if (c != col >> 1) continue;
-#pragma unroll
-                            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                                for (int k = 0; k < 2; ++k)
-                                    if (t < seen[mt][k])
-#pragma unroll
-                                        for (int j = 0; j < NT; ++j) {
-                                            if (col & 1) o[mt][j][2 * k + 1] = NAN;
-                                            else o[mt][j][2 * k] = NAN;
-                                        }
-                        }
-                        __syncwarp();
-                    }
-                }
-                sc[nt] = scales2(sb[0] | sb[1] << 8);
+                sc[nt] = scales2(vsc[4 * ms + 2 * nt] | vsc[4 * ms + 2 * nt + 1] << 8);
             }
 #pragma unroll
             for (int w = 0; w < D / 64; ++w) {
@@ -455,10 +470,6 @@ __global__ void __launch_bounds__(32 * kWarps4, MT == 1 ? 3 : 2) attend_kernel(c
         }
         __syncwarp();  // the stage is free
     }
-    if (failed) {  // wait for what is still in flight, within the same bound
-        if (lane == 0) report_opt(a.err, DEV_PIPE_TIMEOUT, b, h, t_begin);
-        for (int s = 0; s < kStages; ++s) mbar_wait(bar + s, 0), mbar_wait(bar + s, 1);
-    }
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -467,7 +478,7 @@ __global__ void __launch_bounds__(32 * kWarps4, MT == 1 ? 3 : 2) attend_kernel(c
             l[mt][k] += __shfl_xor_sync(0xffffffffu, l[mt][k], 2);
             if (c == 0) sml[(warp * MT + mt) * 16 + g + 8 * k] = make_float2(m[mt][k], l[mt][k]);
         }
-    if (__syncthreads_or(failed)) return;
+    __syncthreads();
 
     // Join the warps: each scales its rows to the common maximum, then the sums are added from shared memory.
     float *so = reinterpret_cast<float *>(sm);
@@ -481,15 +492,17 @@ __global__ void __launch_bounds__(32 * kWarps4, MT == 1 ? 3 : 2) attend_kernel(c
             float top = -INFINITY;
 #pragma unroll
             for (int w = 0; w < kWarps4; ++w) top = fmaxf(top, sml[(w * MT + mt) * 16 + g + 8 * k].x);
-            const float fac = m[mt][k] == -INFINITY ? 1.f : ex2(m[mt][k] - top);
+            const float scale = m[mt][k] == -INFINITY ? 1.f : ex2(m[mt][k] - top);
             float *dst = so + (warp * 16 + g + 8 * k) * kRow;
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
+            for (int e = 0; e < 2; ++e) {
+                const float fac = (nan_cols >> (2 * (2 * mt + k) + e)) & 1 ? NAN : scale;
 #pragma unroll
                 for (int j = 0; j < NT; j += 4)
                     *reinterpret_cast<float4 *>(dst + (2 * c + e) * (D / 8) + j) =
                         make_float4(o[mt][j][2 * k + e] * fac, o[mt][j + 1][2 * k + e] * fac,
                                     o[mt][j + 2][2 * k + e] * fac, o[mt][j + 3][2 * k + e] * fac);
+            }
         }
         __syncthreads();
         // 8 threads a row, D / 8 channels each
@@ -504,11 +517,14 @@ __global__ void __launch_bounds__(32 * kWarps4, MT == 1 ? 3 : 2) attend_kernel(c
         }
         float acc[D / 8];
 #pragma unroll
-        for (int j = 0; j < D / 8; ++j) {
-            acc[j] = 0.f;
+        for (int j = 0; j < D / 8; ++j) acc[j] = 0.f;
+#pragma unroll 1
+        for (int w = 0; w < kWarps4; ++w)
 #pragma unroll
-            for (int w = 0; w < kWarps4; ++w) acc[j] += so[(w * 16 + row) * kRow + at + j];
-        }
+            for (int j = 0; j < D / 8; j += 4) {
+                const float4 v = *reinterpret_cast<const float4 *>(so + (w * 16 + row) * kRow + at + j);
+                acc[j] += v.x; acc[j + 1] += v.y; acc[j + 2] += v.z; acc[j + 3] += v.w;
+            }
         const int grow = row0 + 16 * mt + row;
         if (grow >= rows) continue;
         if (ns == 1) {
@@ -552,6 +568,7 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttendArgs a) {
     for (int r = threadIdx.x / TPR; r < min(RT, rows - row0); r += 256 / TPR) {
         const int at = (threadIdx.x % TPR) * 4;
         float top = -INFINITY, sum = 0.f;
+#pragma unroll 4
         for (int s = 0; s < ns; ++s) top = fmaxf(top, ml[(unit + s) * RT + r].x);
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int s = 0; s < ns; ++s) {
@@ -570,6 +587,8 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttendArgs a) {
 }
 
 float score_scale(float sm_scale, float k_scale) { return sm_scale * k_scale * 1.4426950408889634f; }
+
+constexpr int64_t kMaxL = 1024, kWaves = 4;
 
 // Sizes of the launch.  Row tiles of 32 where a request can have more than 16 rows.
 struct Plan {
@@ -591,13 +610,14 @@ bool attend_plan(const rssm_kv4_config *c, const rssm_attend_config *t, Kv4Args 
     if (tiles * kv->Hk > 65535) return false;
     int64_t seq = (int64_t)t->max_pages * kv->ps;
     if (t->max_seq < seq) seq = t->max_seq;
-    // Split the context where the tiles alone do not fill the machine (148 SMs, 3 CTAs each) twice over.
-    const int64_t units = (int64_t)t->batch * kv->Hk * tiles, want = 148 * 3 * 2;
-    int64_t splits = (want + units - 1) / units, most = (seq + 255) / 256;
-    if (splits > most) splits = most;
-    if (splits < 1) splits = 1;
-    const int64_t L = ((seq + splits - 1) / splits + 127) / 128 * 128;
-    splits = (seq + L - 1) / L;
+    // Tokens of one CTA: a share of the work that fills the machine (148 SMs, 3 CTAs each) several times over,
+    // between 256 (a shorter one is all start and join) and kMaxL (a longer one makes a long tail).
+    const int64_t units = (int64_t)t->batch * kv->Hk * tiles, want = 148 * 3 * kWaves;
+    int64_t L = (seq * units + want - 1) / want;
+    L = L < 256 ? 256 : L > kMaxL ? kMaxL : L;
+    if (tiles > 4) L = seq;  // a prompt chunk: its tiles fill the machine
+    L = (L + 127) / 128 * 128;
+    const int64_t splits = (seq + L - 1) / L;
     p->tiles = (int)tiles;
     p->splits = (int)splits;
     p->L = (int)L;

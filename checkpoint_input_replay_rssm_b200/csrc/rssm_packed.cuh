@@ -8,7 +8,8 @@ namespace rssm {
 
 enum PackedErr : int { DEV_BAD_LENGTHS = 4, DEV_NO_PAGES = 5, DEV_BAD_PAGE = 6 };
 
-__device__ __forceinline__ void report_opt(int32_t *err, int code, int b, int h, int value) {
+// Out of line: it is off every kernel's path, and its code would lie between what is on it.
+static __device__ __noinline__ void report_opt(int32_t *err, int code, int b, int h, int value) {
     if (err) report(err, code, b, h, value);
 }
 
@@ -19,6 +20,6 @@ __device__ __forceinline__ bool packed_rows(const int32_t *cu, int b, int rows, 
     return r0 >= 0 && r0 <= r1 && r1 <= rows;
 }
 
-inline bool aligned16(const void *p) { return ((uintptr_t)p & 15) == 0; }
+static inline bool aligned16(const void *p) { return ((uintptr_t)p & 15) == 0; }
 
 }  // namespace rssm
