@@ -11,22 +11,13 @@
 // the chain through the reduction bounds this kernel, not HBM.  A row's columns lie
 // over 8 lanes in float4 pieces, 4 lane groups of 2 rows each.  Tokens are staged 16 at
 // a time in shared memory (fp32), the next 16 in flight meanwhile.
+#include "rssm_gdn_prefill.h"
 #include "rssm_internal.h"
 #include "rssm_packed.cuh"
 
 namespace rssm {
 
 namespace {
-
-struct GdnPreArgs {
-    int B, H, P, tokens;
-    const void *q, *k, *v;      // [tokens][H][N], [tokens][H][N], [tokens][H][P]
-    const float *alpha, *beta;  // [tokens][H]
-    const int32_t *cu;          // [B + 1]
-    const float *S0;            // [B][H][P][N] or nullptr
-    float *y, *S_out;
-    int32_t *err;
-};
 
 constexpr int kRecWarps = 4;             // 8 state rows each
 constexpr int kRecRows = 8 * kRecWarps;  // rows of one CTA
@@ -181,6 +172,11 @@ bool gdn_prefill_valid(const rssm_gdn_prefill_config *c) {
            (c->input_dtype == RSSM_F32 || c->input_dtype == RSSM_BF16) && c->tokens >= 1;
 }
 
+// The chunked form takes what its tiles are made for.
+bool gdn_chunked(const rssm_gdn_prefill_config &c) {
+    return c.dstate == 128 && c.input_dtype == RSSM_BF16 && c.headdim % 64 == 0;
+}
+
 }  // namespace
 
 }  // namespace rssm
@@ -188,7 +184,8 @@ bool gdn_prefill_valid(const rssm_gdn_prefill_config *c) {
 extern "C" {
 
 RSSM_API size_t rssm_gdn_prefill_workspace_bytes(const rssm_gdn_prefill_config *cfg) {
-    return 0;
+    using namespace rssm;
+    return gdn_prefill_valid(cfg) && gdn_chunked(*cfg) ? gdn_chunk_bytes(cfg->batch, cfg->nheads, cfg->tokens) : 0;
 }
 
 RSSM_API rssm_status rssm_gdn_prefill(const rssm_gdn_prefill_config *cfg, const float *S0, const rssm_inputs *in,
@@ -205,8 +202,9 @@ RSSM_API rssm_status rssm_gdn_prefill(const rssm_gdn_prefill_config *cfg, const 
     if (need && (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 255))) return RSSM_EINVAL;
     const rssm_gdn_prefill_config &c = *cfg;
     const GdnPreArgs a{c.batch, c.nheads, c.headdim, c.tokens, in->q, in->k, in->v, in->alpha, in->beta,
-                       cu, S0, y, S_out, dev_error};
-    const cudaError_t e = c.input_dtype == RSSM_BF16 ? launch_recurrent<__nv_bfloat16>(a, c.dstate, (cudaStream_t)stream)
+                       cu, S0, y, S_out, (uint8_t *)workspace, dev_error};
+    const cudaError_t e = gdn_chunked(c) ? gdn_chunk_launch(a, (cudaStream_t)stream)
+                          : c.input_dtype == RSSM_BF16 ? launch_recurrent<__nv_bfloat16>(a, c.dstate, (cudaStream_t)stream)
                                                      : launch_recurrent<float>(a, c.dstate, (cudaStream_t)stream);
     return e == cudaSuccess ? RSSM_OK : RSSM_ECUDA;
 }

@@ -588,7 +588,7 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttendArgs a) {
 
 float score_scale(float sm_scale, float k_scale) { return sm_scale * k_scale * 1.4426950408889634f; }
 
-constexpr int64_t kMaxL = 1024, kWaves = 4;
+constexpr int64_t kMaxL = 2048, kWaves = 2;
 
 // Sizes of the launch.  Row tiles of 32 where a request can have more than 16 rows.
 struct Plan {
