@@ -9,10 +9,10 @@
 //   S <- 2^{Lam_C} S + sum_j 2^{Lam_C - Lam_j} u_j k_j^T
 // What does not meet the state is one kernel over all chunks at once: it leaves the 128 x 64
 // matrix [T diag(beta); M T diag(beta)] for the other, which walks the chunks of one
-// (request, head, 64 rows of the state) with three products a chunk, all with 128 rows:
-//   [K; Q] S^T        (128 x 128 x 64: the K rows give R, the Q rows the first part of O)
-//   [T b; M T b] R    (128 x 64 x 64:  the K rows give U, the Q rows the second part of O)
-//   K^T (w U)         (128 x 64 x 64 onto the state, which stays in tensor memory, transposed)
+// (request, head, 128 rows of the state) with three products a chunk:
+//   S [K; Q]^T       (128 x 128 x 128: the K columns give R, the Q columns the first part of O)
+//   R^T [T b; M T b]^T  (128 x 128 x 64: the K columns give U, the Q columns the second part of O)
+//   (w U)^T K        (128 x 128 x 64 onto the state, which stays in tensor memory)
 // q, k and v are bf16 and enter exactly; fp32 operands enter as a (hi, lo) bf16 pair, which
 // leaves 2^-17 of the value, and the lo lo product is dropped (2^-18): near-fp32 accuracy at
 // two or three bf16 products, where one tf32 product would leave 2^-11.
@@ -37,28 +37,42 @@ namespace {
 
 constexpr int kC = 64;                  // chunk
 constexpr int kDk = 128;                // state columns (N)
-constexpr int kPs = 64;                 // state rows a scan CTA owns
 constexpr int kTile = 128 * kC * 2;     // [128 x 64] bf16
 constexpr int kSlot = 2 * kTile + 512;  // hi, lo, then 2^Lam_i and 2^{Lam_C - Lam_i} fp32
 
-__device__ __forceinline__ uint32_t bf2(__nv_bfloat16 a, __nv_bfloat16 b) {
-    return (uint32_t)__bfloat16_as_ushort(a) | (uint32_t)__bfloat16_as_ushort(b) << 16;
+// Eight fp32 values as 16-byte chunks of their (hi, lo) parts.  The conversions are the two-value ones: the
+// one-value form runs at an eighth of their rate.
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
 }
-// Eight fp32 values as 16-byte chunks of their (hi, lo) parts.
 __device__ __forceinline__ void split8(const float *v, uint4 &hi, uint4 &lo) {
     uint32_t *ph = &hi.x, *pl = &lo.x;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        __nv_bfloat16 h0, l0, h1, l1;
-        split_bf16(v[2 * e], h0, l0);
-        split_bf16(v[2 * e + 1], h1, l1);
-        ph[e] = bf2(h0, h1);
-        pl[e] = bf2(l0, l1);
+        const uint32_t h = bf16x2(v[2 * e], v[2 * e + 1]);
+        ph[e] = h;
+        pl[e] = bf16x2(v[2 * e] - __uint_as_float(h << 16), v[2 * e + 1] - __uint_as_float(h & 0xffff0000u));
     }
+}
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
 }
 __device__ __forceinline__ void bulk_s2g(void *dst, const void *src, uint32_t bytes) {
     asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
                  : "memory");
+}
+
+// Wait for a phase, bounded in cycles (2 s at 2 GHz).
+__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (!mbar_try_wait(bar, parity))
+        if (clock64() - t0 > 4000000000ll) return false;
+    return true;
 }
 
 // ---------------------------------------------------------------- chunk operands
@@ -172,7 +186,7 @@ __global__ void __launch_bounds__(128, 3) gdn_chunk_kernel(const GdnPreArgs a) {
             out[kC + i] = exp2f((lamh[kC - 1] - li) + (laml[kC - 1] - ll));
         }
         __syncwarp();
-        failed = !mbar_wait(bar, 0);
+        failed = !bar_wait(bar, 0);
         failed = __syncthreads_or(failed);
         tc_fence_after();
         if (!failed) {
@@ -188,7 +202,7 @@ __global__ void __launch_bounds__(128, 3) gdn_chunk_kernel(const GdnPreArgs a) {
                     tmem_ld16(base + j0, gv);
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
-                        gv[j] = j0 + j < lim ? bi * exp2f((li - lamh[j0 + j]) + (ll - laml[j0 + j])) * gv[j] : 0.f;
+                        gv[j] = j0 + j < lim ? bi * ex2((li - lamh[j0 + j]) + (ll - laml[j0 + j])) * gv[j] : 0.f;
                 } else {
 #pragma unroll
                     for (int j = 0; j < 16; ++j) gv[j] = 0.f;
@@ -302,7 +316,7 @@ __global__ void __launch_bounds__(128, 3) gdn_chunk_kernel(const GdnPreArgs a) {
                 umma_commit(bar);
             }
             __syncwarp();
-            failed = !mbar_wait(bar, 1);
+            failed = !bar_wait(bar, 1);
             failed = __syncthreads_or(failed);
             tc_fence_after();
             if (!failed) {
@@ -337,216 +351,269 @@ __global__ void __launch_bounds__(128, 3) gdn_chunk_kernel(const GdnPreArgs a) {
 }
 
 // ---------------------------------------------------------------- scan over the chunks
+// Everything is transposed, so that a tensor-memory lane is a state row p and a thread meets one row only: the
+// state, the products Y^T = S [K; Q]^T and Z^T = R^T [T b; M T b]^T, and the left operands, which live in tensor
+// memory too (bf16 pairs) and never pass through shared memory.  v and o are then read and written along p, whole
+// lines at a time.
+// Columns: S fp32 (128); Y^T (K tokens, Q tokens; Z^T of the K tokens takes the first's place); S hi and lo (128), whose
+// place (w U)^T hi and lo take; Z^T of the Q tokens (64); R^T hi and lo (64).
+// The chain from state to state is S -> Y_k -> R -> Z_k -> U -> S; what only the outputs need is issued behind it
+// and read while the next chunk's first product runs.
+constexpr uint32_t kTmS = 0, kTmY = 128, kTmA = 256, kTmU = 256, kTmZq = 384, kTmR = 448;
 struct ScanSmem {
-    static constexpr int kKQ = 0;                 // [K; Q] 128 x 128 bf16
-    static constexpr int kOp = kKQ + 2 * kTile;   // [T b; M T b] hi, lo, then the decays
-    static constexpr int kDec = kOp + 2 * kTile;
-    static constexpr int kS = kDec + 1024;        // S hi, lo [128 n][64 p]; then R hi, lo and w U hi, lo [64 j][64 p]
-    static constexpr int kBar = kS + 2 * kTile;
-    static constexpr int kBytes = kBar + 32;
+    static constexpr int kKQ = 0;                     // [K; Q] 128 x 128 bf16, two buffers
+    static constexpr int kOp = kKQ + 2 * 2 * kTile;   // [T b; M T b] hi, lo and the decays, two buffers
+    static constexpr int kOpStep = 2 * kTile + 1024;
+    static constexpr int kV = kOp + 2 * kOpStep;      // v [64 tokens][128 p] bf16, two buffers
+    static constexpr int kO = kV + 2 * kC * 256;      // o [64 tokens][128 p] fp32
+    static constexpr int kBar = kO + kC * 512;
+    static constexpr int kBytes = kBar + 64;
 };
-constexpr int kRTile = kC * kPs * 2;  // one part of R or w U
-constexpr int kScanThreads = 256;
+constexpr int kScanThreads = 512;  // 4 column groups: 32 state columns, 16 K and 16 Q tokens each
+enum ScanBar { kBarYk, kBarZk, kBarS, kBarZq, kBarOp /* two */, kBarN = kBarOp + 2 };
 
-__global__ void __launch_bounds__(kScanThreads, 2) gdn_scan_kernel(const GdnPreArgs a) {
+__global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const GdnPreArgs a) {
     using L = ScanSmem;
     extern __shared__ __align__(1024) uint8_t raw[];
     uint8_t *sm = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
-    uint8_t *sKQ = sm + L::kKQ, *sOp = sm + L::kOp, *sS = sm + L::kS;
-    float *dec = reinterpret_cast<float *>(sm + L::kDec);  // 2^Lam_i, then 2^{Lam_C - Lam_i}
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + L::kBar);
-    uint32_t *tslot = reinterpret_cast<uint32_t *>(bar + 2);
-    const int tid = threadIdx.x, warp = tid >> 5;
-    const int row = tid & 127;               // tensor-memory lane: token (K rows, Q rows) or state column n
-    const int pl = (tid >> 7) * (kPs / 2);   // this thread's 32 of the CTA's 64 state rows
-    const int slices = a.P / kPs, h = blockIdx.x / slices, p0 = (blockIdx.x % slices) * kPs, b = blockIdx.y, H = a.H;
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(bar + kBarN);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, row = tid & 127, grp = tid >> 7;
+    const int slices = (a.P + 127) / 128, h = blockIdx.x / slices, p = (blockIdx.x % slices) * 128 + row, b = blockIdx.y;
+    const int H = a.H, P = a.P;
     int r0, r1;
     if (!packed_rows(a.cu, b, a.tokens, r0, r1)) {
         if (tid == 0) report_opt(a.err, DEV_BAD_LENGTHS, b, h, r1);
         return;
     }
-    const int64_t head = (int64_t)b * H + h;
-    if (warp == 0) tmem_alloc(tslot, 256);
+    const bool on = p < P;
+    if (warp == 0) tmem_alloc(tslot, 512);
     if (tid == 0) {
-        mbar_init(bar, 1);
+        for (int i = 0; i < kBarN; ++i) mbar_init(bar + i, 1);
         mbar_init_fence();
+    }
+    const int nchunks = (r1 - r0 + kC - 1) / kC;
+    const uint8_t *ws = a.ws + ((int64_t)(r0 / kC + b) * H + h) * kSlot;
+    const int64_t ws_step = (int64_t)H * kSlot;
+
+    // K and Q rows of a chunk: 16 lanes a row, this thread's rows 32 apart (4096 bytes in shared memory).
+    const int lt = tid >> 4;
+    const uint32_t ld_dst = sw128_chunk(lt, tid & 15, 128);
+    const int64_t ld_row = (int64_t)H * kDk * 2, ld_at = ((int64_t)(r0 + lt) * H + h) * kDk * 2 + 16 * (tid & 15);
+    auto load_rows = [&](int cc) {
+        const int left = r1 - (r0 + cc * kC) - lt;
+        uint8_t *dst = sm + L::kKQ + (cc & 1) * 2 * kTile + ld_dst;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int t = 32 * (r & 1);
+            if (t < left)
+                cp_async16(dst + 4096 * r, reinterpret_cast<const uint8_t *>(r < 2 ? a.k : a.q) + ld_at + (cc * kC + t) * ld_row);
+            else
+                *reinterpret_cast<uint4 *>(dst + 4096 * r) = make_uint4(0, 0, 0, 0);
+        }
+    };
+    auto load_op = [&](int cc) {  // one thread
+        uint64_t *br = bar + kBarOp + (cc & 1);
+        mbar_arrive_expect_tx(br, kSlot);
+        bulk_g2s(sm + L::kOp + (cc & 1) * L::kOpStep, ws + cc * ws_step, kSlot, br);
+    };
+    // v and o pass through shared memory and meet global memory in runs of 16 bytes a lane along p: a warp's
+    // accesses of 2 and 4 bytes a lane took 1600 and 2500 cycles a chunk, a bulk copy a token about as long.
+    const int64_t v_row = (int64_t)H * P;
+    const int p_base = p - row, p_here = min(128, P - p_base);  // state rows of this CTA
+    auto load_v = [&](int cc) {
+        const int t0 = r0 + cc * kC, at = (tid & 15) * 8;
+        const __nv_bfloat16 *src = reinterpret_cast<const __nv_bfloat16 *>(a.v) + (int64_t)t0 * v_row + (int64_t)h * P + p_base + at;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int t = lt + 32 * r;
+            if (t0 + t < r1 && at < p_here) cp_async16(sm + L::kV + ((cc & 1) * kC + t) * 256 + 2 * at, src + t * v_row);
+        }
+    };
+    auto store_o = [&](int cc) {
+        const int t0 = r0 + cc * kC, at = lane * 4;
+        float *dst = a.y + (int64_t)t0 * v_row + (int64_t)h * P + p_base + at;
+        const float *src = reinterpret_cast<const float *>(sm + L::kO) + at;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int t = warp + 16 * r;
+            if (t0 + t < r1 && at < p_here) *reinterpret_cast<float4 *>(dst + t * v_row) = *reinterpret_cast<const float4 *>(src + t * 128);
+        }
+    };
+    if (nchunks > 0) {
+        load_rows(0);
+        load_v(0);
+    }
+    float s[32];  // S[p][32 grp ..]
+    const int64_t s_at = (((int64_t)b * H + h) * P + p) * kDk + 32 * grp;
+#pragma unroll
+    for (int j = 0; j < 32; j += 4) {
+        const float4 x = on && a.S0 ? *reinterpret_cast<const float4 *>(a.S0 + s_at + j) : make_float4(0.f, 0.f, 0.f, 0.f);
+        s[j] = x.x; s[j + 1] = x.y; s[j + 2] = x.z; s[j + 3] = x.w;
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tslot, base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-    const uint32_t cY = 0, cZ = kPs, cS = 2 * kPs;
-    const int nchunks = (r1 - r0 + kC - 1) / kC;
-    const uint8_t *ws = a.ws + ((int64_t)(r0 / kC + b) * H + h) * kSlot;
-    const int64_t ws_step = (int64_t)H * kSlot;
+    if (tid == 0 && nchunks > 0) load_op(0);
 
-    // Parts of the next chunk's operands: K rows, Q rows, the matrix and decays.
-    auto load_rows = [&](int cc, bool q) {
-        const int t0 = r0 + cc * kC, Lc = min(kC, r1 - t0);
-        const uint8_t *src = reinterpret_cast<const uint8_t *>(q ? a.q : a.k);
-        for (int i = tid; i < kC * 16; i += kScanThreads) {
-            const int t = i >> 4, ch = i & 15;
-            uint8_t *dst = sKQ + sw128_chunk(q ? kC + t : t, ch, 128);
-            if (t < Lc) cp_async16(dst, src + (((int64_t)(t0 + t) * H + h) * kDk) * 2 + 16 * ch);
-            else *reinterpret_cast<uint4 *>(dst) = make_uint4(0, 0, 0, 0);
-        }
-    };
-    auto load_op = [&](int cc) {
-        const uint8_t *src = ws + cc * ws_step;
-        for (int i = tid; i < kSlot / 16; i += kScanThreads) cp_async16(sOp + 16 * i, src + 16 * i);
-    };
-    uint4 vreg[4];  // v of this thread's token and 32 state rows (threads of K rows)
-    auto load_v = [&](int cc) {
-        const int t = r0 + cc * kC + row;
-        const bool live = row < kC && t < r1;
-        const uint4 *src = reinterpret_cast<const uint4 *>(reinterpret_cast<const __nv_bfloat16 *>(a.v) +
-                                                           ((int64_t)t * H + h) * a.P + p0 + pl);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) vreg[k] = live ? src[k] : make_uint4(0, 0, 0, 0);
-    };
-
-    float s[32];  // S^T[n = row][pl ..]
-#pragma unroll
-    for (int j = 0; j < 32; ++j) s[j] = a.S0 ? a.S0[(head * a.P + p0 + pl + j) * kDk + row] : 0.f;
-    if (nchunks > 0) {
-        load_rows(0, false);
-        load_rows(0, true);
-        load_op(0);
-        load_v(0);
-    }
-    cp_async_commit();
-
-    uint32_t phase = 0;
+    const uint32_t smem0 = smem_u32(sm);
     bool failed = false;
-    // All of the CTA's writes are visible to the tensor cores; thread 0 then issues.
+    // Operands written by this thread are in place; true when every wait so far has succeeded.
     auto ready = [&]() {
+        tmem_st_wait();
         fence_async_smem();
         tc_fence_before();
-        __syncthreads();
-        tc_fence_after();
-    };
-    auto wait_mma = [&]() {
-        __syncwarp();
-        if (!mbar_wait(bar, phase & 1)) failed = true;
-        ++phase;
         failed = __syncthreads_or(failed);
         tc_fence_after();
         return !failed;
     };
-    for (int c = 0; c < nchunks; ++c) {
-        const int t0 = r0 + c * kC;
-        // S at the chunk's start as (hi, lo), and 2^{Lam_C} S into tensor memory.
-        if (c > 0) tmem_ld32(base + cS + pl, s);
+    auto wait_for = [&](int which, int parity) {
+        __syncwarp();
+        if (!bar_wait(bar + which, parity)) failed = true;
+        tc_fence_after();
+    };
+    // 16 fp32 as 8 columns of hi and of lo.
+    auto put16 = [&](const float *x, uint32_t hi_at, uint32_t lo_at) {
+        alignas(16) uint32_t hi[8], lo[8];
+        split8(x, *reinterpret_cast<uint4 *>(hi), *reinterpret_cast<uint4 *>(lo));
+        split8(x + 8, *reinterpret_cast<uint4 *>(hi + 4), *reinterpret_cast<uint4 *>(lo + 4));
+        tmem_st_u32(base + hi_at, hi);
+        tmem_st_u32(base + lo_at, lo);
+    };
+    float yq[16];
+    // O of chunk cc: 2^Lam (S q) + Z.
+    auto write_o = [&](int cc) {
+        wait_for(kBarZq, cc & 1);
+        float z[16];
+        tmem_ld16(base + kTmZq + 16 * grp, z);
+        const float4 *e = reinterpret_cast<const float4 *>(sm + L::kOp + (cc & 1) * L::kOpStep + 2 * kTile + 64 * grp);
+        float *dst = reinterpret_cast<float *>(sm + L::kO) + 16 * grp * 128 + row;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            uint4 hi, lo;
-            split8(s + 8 * k, hi, lo);
-            const uint32_t off = sw128_chunk(row, (pl >> 3) + k, 128);
-            *reinterpret_cast<uint4 *>(sS + off) = hi;
-            *reinterpret_cast<uint4 *>(sS + kTile + off) = lo;
+            const float4 d = e[k];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) dst[(4 * k + j) * 128] = fmaf((&d.x)[j], yq[4 * k + j], z[4 * k + j]);
         }
+    };
+    int c = 0;
+    for (; c < nchunks; ++c) {
+        const int par = c & 1;
+        // descriptors: K (Q's rows lie 8192 bytes on) along its columns, K along its tokens, the matrix
+        const uint32_t kq = sw128_desc_lo(smem0 + L::kKQ + par * 2 * kTile), kt = sw128_desc_lo(smem0 + L::kKQ + par * 2 * kTile, kTile);
+        const uint32_t op = sw128_desc_lo(smem0 + L::kOp + par * L::kOpStep);
+        const float *dec = reinterpret_cast<const float *>(sm + L::kOp + par * L::kOpStep + 2 * kTile);
+        // S at the chunk's start as (hi, lo).
+        if (c > 0) {
+            wait_for(kBarS, par ^ 1);
+            tmem_ld32(base + kTmS + 32 * grp, s);
+        }
+        put16(s, kTmA + 16 * grp, kTmA + 64 + 16 * grp);
+        put16(s + 16, kTmA + 16 * grp + 8, kTmA + 64 + 16 * grp + 8);
         cp_async_wait_all();
-        ready();
-        if (tid == 0) {
-            const uint32_t kq = smem_u32(sKQ);
-            for (int hl = 0; hl < 2; ++hl)
-                for (int ks = 0; ks < kDk / 16; ++ks)
-                    umma_bf16(tmem + cY, sw128_desc(kq, 128, ks), sw128_mn_desc(smem_u32(sS) + hl * kTile, 1024, ks),
-                              idesc_bf16_f32_mn(128, kPs, false, true), hl > 0 || ks > 0);
-            umma_commit(bar);
+        if (!ready()) break;
+        if (warp == 0 && elect_one()) {  // Y^T = S [K; Q]^T, the K tokens first
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+#pragma unroll
+                for (int hl = 0; hl < 2; ++hl)
+#pragma unroll
+                    for (int ks = 0; ks < kDk / 16; ++ks)
+                        umma_bf16_ts(tmem + kTmY + q * kC, tmem + kTmA + 64 * hl + 8 * ks,
+                                     sw128_desc_of(kq + (q * kC * 128 + (ks >> 2) * kTile + (ks & 3) * 32) / 16),
+                                     idesc_bf16_f32(128, kC), hl > 0 || ks > 0);
+                if (q == 0) umma_commit(bar + kBarYk);
+            }
         }
-        {
+        if (c > 0) write_o(c - 1);
+        wait_for(kBarOp + par, (c >> 1) & 1);
+        {  // 2^{Lam_C} S back into tensor memory
             const float d = dec[kC - 1];
 #pragma unroll
             for (int j = 0; j < 32; ++j) s[j] *= d;
-            tmem_st32(base + cS + pl, s);
-        }
-        const float di = dec[row & 63];
-        if (!wait_mma()) break;
-        // R = V - 2^Lam (K S^T), over S's place (its product has completed).
-        float yv[32];
-        tmem_ld32(base + cY + pl, yv);
-        if (row < kC) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                float r[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const uint32_t w = (&vreg[k].x)[e >> 1];
-                    r[e] = fmaf(-di, yv[8 * k + e], bf16_bits_to_float((e & 1) ? w >> 16 : w & 0xffff));
-                }
-                uint4 hi, lo;
-                split8(r, hi, lo);
-                const uint32_t off = sw128_chunk(row, (pl >> 3) + k, kC);
-                *reinterpret_cast<uint4 *>(sS + off) = hi;
-                *reinterpret_cast<uint4 *>(sS + kRTile + off) = lo;
-            }
-        }
-        ready();
-        if (tid == 0) {
-            const uint32_t op = smem_u32(sOp), r = smem_u32(sS);
-            for (int pr = 0; pr < 3; ++pr)
-                for (int ks = 0; ks < kC / 16; ++ks)
-                    umma_bf16(tmem + cZ, sw128_desc(op + (pr == 2 ? kTile : 0), 128, ks),
-                              sw128_mn_desc(r + (pr == 1 ? kRTile : 0), 1024, ks),
-                              idesc_bf16_f32_mn(128, kPs, false, true), pr > 0 || ks > 0);
-            umma_commit(bar);
+            tmem_st32(base + kTmS + 32 * grp, s);
         }
         if (c + 1 < nchunks) {
-            load_rows(c + 1, true);  // Q's rows are done with
+            load_rows(c + 1);
             load_v(c + 1);
         }
-        const float wi = dec[kC + (row & 63)];
-        if (!wait_mma()) break;
-        float zv[32];
-        tmem_ld32(base + cZ + pl, zv);
-        if (row < kC) {  // w U
+        wait_for(kBarYk, par);
+        // R^T = V^T - Y^T 2^Lam; what lies behind the prompt is 0.
+        float x[16];
+        tmem_ld16(base + kTmY + 16 * grp, x);
+        const uint16_t *v = reinterpret_cast<const uint16_t *>(sm + L::kV + par * kC * 256) + 16 * grp * 128 + row;
+        const int live = on ? r1 - (r0 + c * kC) - 16 * grp : 0;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                float u[8];
+        for (int k = 0; k < 4; ++k) {
+            const float4 d = reinterpret_cast<const float4 *>(dec + 16 * grp)[k];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) u[e] = wi * zv[8 * k + e];
-                uint4 hi, lo;
-                split8(u, hi, lo);
-                const uint32_t off = sw128_chunk(row, (pl >> 3) + k, kC);
-                *reinterpret_cast<uint4 *>(sS + kTile + off) = hi;
-                *reinterpret_cast<uint4 *>(sS + kTile + kRTile + off) = lo;
-            }
+            for (int j = 0; j < 4; ++j)
+                x[4 * k + j] = 4 * k + j < live ? fmaf(-(&d.x)[j], x[4 * k + j], bf16_bits_to_float(v[(4 * k + j) * 128])) : 0.f;
         }
-        ready();
-        if (tid == 0) {
-            const uint32_t kq = smem_u32(sKQ), u = smem_u32(sS) + kTile;
-            for (int hl = 0; hl < 2; ++hl)
+        put16(x, kTmR + 8 * grp, kTmR + 32 + 8 * grp);
+        if (!ready()) break;
+        if (warp == 0 && elect_one()) {  // Z^T = R^T (T b)^T
+#pragma unroll
+            for (int pr = 0; pr < 3; ++pr)
+#pragma unroll
                 for (int ks = 0; ks < kC / 16; ++ks)
-                    umma_bf16(tmem + cS, sw128_mn_desc(kq, kTile, ks), sw128_mn_desc(u + hl * kRTile, 1024, ks),
-                              idesc_bf16_f32_mn(128, kPs, true, true), true);
-            umma_commit(bar);
+                    umma_bf16_ts(tmem + kTmY, tmem + kTmR + (pr == 2 ? 32 : 0) + 8 * ks,
+                                 sw128_desc_of(op + ((pr == 1 ? kTile : 0) + ks * 32) / 16), idesc_bf16_f32(128, kC),
+                                 pr > 0 || ks > 0);
+            umma_commit(bar + kBarZk);
+            if (c + 1 < nchunks) load_op(c + 1);  // every thread has read the decays of chunk c - 1
         }
-        if (row >= kC) {  // O
-            const int t = t0 + row - kC;
-            if (t < r1) {
-                float4 *dst = reinterpret_cast<float4 *>(a.y + ((int64_t)t * H + h) * a.P + p0 + pl);
+        if (c > 0) store_o(c - 1);
+        wait_for(kBarZk, par);
+        tmem_ld16(base + kTmY + 16 * grp, x);
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    dst[k] = make_float4(fmaf(di, yv[4 * k], zv[4 * k]), fmaf(di, yv[4 * k + 1], zv[4 * k + 1]),
-                                         fmaf(di, yv[4 * k + 2], zv[4 * k + 2]), fmaf(di, yv[4 * k + 3], zv[4 * k + 3]));
-            }
+        for (int k = 0; k < 4; ++k) {
+            const float4 w = reinterpret_cast<const float4 *>(dec + kC + 16 * grp)[k];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[4 * k + j] *= (&w.x)[j];
         }
-        if (c + 1 < nchunks) load_op(c + 1);
-        if (!wait_mma()) break;
-        if (c + 1 < nchunks) load_rows(c + 1, false);
+        put16(x, kTmU + 8 * grp, kTmU + 32 + 8 * grp);
+        tmem_ld16(base + kTmY + kC + 16 * grp, yq);
+        if (!ready()) break;
+        if (warp == 0 && elect_one()) {
+#pragma unroll
+            for (int hl = 0; hl < 2; ++hl)  // S += (w U)^T K
+#pragma unroll
+                for (int ks = 0; ks < kC / 16; ++ks)
+                    umma_bf16_ts(tmem + kTmS, tmem + kTmU + 32 * hl + 8 * ks, sw128_desc_of(kt + ks * 2048 / 16),
+                                 idesc_bf16_f32_mn(128, kDk, false, true), true);
+            umma_commit(bar + kBarS);
+#pragma unroll
+            for (int pr = 0; pr < 3; ++pr)  // Z^T of the Q tokens = R^T (M T b)^T
+#pragma unroll
+                for (int ks = 0; ks < kC / 16; ++ks)
+                    umma_bf16_ts(tmem + kTmZq, tmem + kTmR + (pr == 2 ? 32 : 0) + 8 * ks,
+                                 sw128_desc_of(op + (kC * 128 + (pr == 1 ? kTile : 0) + ks * 32) / 16), idesc_bf16_f32(128, kC),
+                                 pr > 0 || ks > 0);
+            umma_commit(bar + kBarZq);
+        }
+    }
+    if (!failed && nchunks > 0) {
+        wait_for(kBarS, (nchunks - 1) & 1);
+        write_o(nchunks - 1);
+        tmem_ld32(base + kTmS + 32 * grp, s);
     }
     cp_async_wait_all();
+    failed = __syncthreads_or(failed);
+    if (!failed && nchunks > 0) store_o(nchunks - 1);
     if (failed) {
-        if (tid == 0) report_opt(a.err, DEV_PIPE_TIMEOUT, b, h, 0);
-    } else {
-        if (nchunks > 0) tmem_ld32(base + cS + pl, s);
+        if (tid == 0) {
+            for (int i = 0; i < 2; ++i) bar_wait(bar + kBarOp + i, 0), bar_wait(bar + kBarOp + i, 1);  // copies still in flight
+            report_opt(a.err, DEV_PIPE_TIMEOUT, b, h, c);
+        }
+    } else if (on) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) a.S_out[(head * a.P + p0 + pl + j) * kDk + row] = s[j];
+        for (int j = 0; j < 32; j += 4)
+            *reinterpret_cast<float4 *>(a.S_out + s_at + j) = make_float4(s[j], s[j + 1], s[j + 2], s[j + 3]);
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 0) tmem_dealloc(tmem, 256);
+    if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
 int64_t slots(int B, int tokens) { return (int64_t)tokens / kC + B + 1; }
@@ -562,7 +629,7 @@ cudaError_t gdn_chunk_launch(const GdnPreArgs &a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     gdn_chunk_kernel<<<dim3((unsigned)slots(a.B, a.tokens), a.H), 128, s1, st>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    gdn_scan_kernel<<<dim3(a.H * (a.P / kPs), a.B), kScanThreads, s2, st>>>(a);
+    gdn_scan_kernel<<<dim3(a.H * ((a.P + 127) / 128), a.B), kScanThreads, s2, st>>>(a);
     return cudaGetLastError();
 }
 

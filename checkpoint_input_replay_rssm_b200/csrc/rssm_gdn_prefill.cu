@@ -174,7 +174,7 @@ bool gdn_prefill_valid(const rssm_gdn_prefill_config *c) {
 
 // The chunked form takes what its tiles are made for.
 bool gdn_chunked(const rssm_gdn_prefill_config &c) {
-    return c.dstate == 128 && c.input_dtype == RSSM_BF16 && c.headdim % 64 == 0;
+    return c.dstate == 128 && c.input_dtype == RSSM_BF16;
 }
 
 }  // namespace
