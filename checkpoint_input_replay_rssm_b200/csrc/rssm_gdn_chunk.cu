@@ -66,12 +66,25 @@ __device__ __forceinline__ void bulk_s2g(void *dst, const void *src, uint32_t by
                  : "memory");
 }
 
-// Wait for a phase, bounded in cycles (2 s at 2 GHz).
+// A wait on a barrier's phase gives up after this many cycles (2 s at 2 GHz).
+constexpr long long kWaitCycles = 4000000000ll;
+
+// try_wait that may sleep for up to 1 ms: a dozen waiting warps that poll take the shared-memory pipe from the
+// warps that work.
+__device__ __forceinline__ bool bar_try(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u)
+        : "memory");
+    return ok != 0;
+}
 __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (bar_try(bar, parity)) return true;
     const long long t0 = clock64();
-    while (!mbar_try_wait(bar, parity))
-        if (clock64() - t0 > 4000000000ll) return false;
+    while (!bar_try(bar, parity))
+        if (clock64() - t0 > kWaitCycles) return false;
     return true;
 }
 
@@ -360,6 +373,12 @@ __global__ void __launch_bounds__(128, 3) gdn_chunk_kernel(const GdnPreArgs a) {
 // The chain from state to state is S -> Y_k -> R -> Z_k -> U -> S; what only the outputs need is issued behind it
 // and read while the next chunk's first product runs.
 constexpr uint32_t kTmS = 0, kTmY = 128, kTmA = 256, kTmU = 256, kTmZq = 384, kTmR = 448;
+//
+// Roles, each a set of warps, meeting on barriers in shared memory only:
+//   8 chain warps   S, R and U of every chunk as operands: 2 a lane quarter, 64 state columns or 32 tokens each
+//   4 output warps  the finished chunk's O
+//   3 input warps   the next chunks' rows into shared memory
+//   1 issuing warp  the products
 struct ScanSmem {
     static constexpr int kKQ = 0;                     // [K; Q] 128 x 128 bf16, two buffers
     static constexpr int kOp = kKQ + 2 * 2 * kTile;   // [T b; M T b] hi, lo and the decays, two buffers
@@ -367,10 +386,21 @@ struct ScanSmem {
     static constexpr int kV = kOp + 2 * kOpStep;      // v [64 tokens][128 p] bf16, two buffers
     static constexpr int kO = kV + 2 * kC * 256;      // o [64 tokens][128 p] fp32
     static constexpr int kBar = kO + kC * 512;
-    static constexpr int kBytes = kBar + 64;
+    static constexpr int kBytes = kBar + 128;
 };
-constexpr int kScanThreads = 512;  // 4 column groups: 32 state columns, 16 K and 16 Q tokens each
-enum ScanBar { kBarYk, kBarZk, kBarS, kBarZq, kBarOp /* two */, kBarN = kBarOp + 2 };
+constexpr int kChainWarps = 8, kOutWarps = 4, kInWarps = 3;
+constexpr int kFirstIn = kChainWarps + kOutWarps, kIssuer = kFirstIn + kInWarps;
+constexpr int kScanThreads = 32 * (kIssuer + 1);
+enum ScanBar {
+    kBarYk, kBarZk, kBarS, kBarZq,  // products done (one phase a chunk)
+    kBarPutS, kBarPutR, kBarPutU,   // operands in place (every chain warp arrives)
+    kBarOut,                        // the output warps meet
+    kBarO,                          // Y and Z of the Q tokens and the decays read (every output warp arrives)
+    kBarIn,                         // a chunk's K, Q and v rows in shared memory, per buffer (every input warp arrives)
+    kBarOp = kBarIn + 2,            // a chunk's matrix and decays, per buffer
+    kBarEnd = kBarOp + 2,           // everything issued, after a failure
+    kBarN
+};
 
 __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const GdnPreArgs a) {
     using L = ScanSmem;
@@ -378,143 +408,230 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const GdnPreA
     uint8_t *sm = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + L::kBar);
     uint32_t *tslot = reinterpret_cast<uint32_t *>(bar + kBarN);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, row = tid & 127, grp = tid >> 7;
-    const int slices = (a.P + 127) / 128, h = blockIdx.x / slices, p = (blockIdx.x % slices) * 128 + row, b = blockIdx.y;
+    volatile int *sfail = reinterpret_cast<volatile int *>(tslot + 1);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int slices = (a.P + 127) / 128, h = blockIdx.x / slices, p_base = (blockIdx.x % slices) * 128, b = blockIdx.y;
     const int H = a.H, P = a.P;
+    const int p_here = min(128, P - p_base);  // state rows of this CTA
     int r0, r1;
     if (!packed_rows(a.cu, b, a.tokens, r0, r1)) {
         if (tid == 0) report_opt(a.err, DEV_BAD_LENGTHS, b, h, r1);
         return;
     }
-    const bool on = p < P;
     if (warp == 0) tmem_alloc(tslot, 512);
     if (tid == 0) {
-        for (int i = 0; i < kBarN; ++i) mbar_init(bar + i, 1);
+        for (int i = 0; i < kBarN; ++i)
+            mbar_init(bar + i, i >= kBarPutS && i <= kBarPutU ? kChainWarps
+                               : i == kBarOut || i == kBarO   ? kOutWarps
+                               : i == kBarIn || i == kBarIn + 1 ? kInWarps : 1);
+        *sfail = 0;
         mbar_init_fence();
-    }
-    const int nchunks = (r1 - r0 + kC - 1) / kC;
-    const uint8_t *ws = a.ws + ((int64_t)(r0 / kC + b) * H + h) * kSlot;
-    const int64_t ws_step = (int64_t)H * kSlot;
-
-    // K and Q rows of a chunk: 16 lanes a row, this thread's rows 32 apart (4096 bytes in shared memory).
-    const int lt = tid >> 4;
-    const uint32_t ld_dst = sw128_chunk(lt, tid & 15, 128);
-    const int64_t ld_row = (int64_t)H * kDk * 2, ld_at = ((int64_t)(r0 + lt) * H + h) * kDk * 2 + 16 * (tid & 15);
-    auto load_rows = [&](int cc) {
-        const int left = r1 - (r0 + cc * kC) - lt;
-        uint8_t *dst = sm + L::kKQ + (cc & 1) * 2 * kTile + ld_dst;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int t = 32 * (r & 1);
-            if (t < left)
-                cp_async16(dst + 4096 * r, reinterpret_cast<const uint8_t *>(r < 2 ? a.k : a.q) + ld_at + (cc * kC + t) * ld_row);
-            else
-                *reinterpret_cast<uint4 *>(dst + 4096 * r) = make_uint4(0, 0, 0, 0);
-        }
-    };
-    auto load_op = [&](int cc) {  // one thread
-        uint64_t *br = bar + kBarOp + (cc & 1);
-        mbar_arrive_expect_tx(br, kSlot);
-        bulk_g2s(sm + L::kOp + (cc & 1) * L::kOpStep, ws + cc * ws_step, kSlot, br);
-    };
-    // v and o pass through shared memory and meet global memory in runs of 16 bytes a lane along p: a warp's
-    // accesses of 2 and 4 bytes a lane took 1600 and 2500 cycles a chunk, a bulk copy a token about as long.
-    const int64_t v_row = (int64_t)H * P;
-    const int p_base = p - row, p_here = min(128, P - p_base);  // state rows of this CTA
-    auto load_v = [&](int cc) {
-        const int t0 = r0 + cc * kC, at = (tid & 15) * 8;
-        const __nv_bfloat16 *src = reinterpret_cast<const __nv_bfloat16 *>(a.v) + (int64_t)t0 * v_row + (int64_t)h * P + p_base + at;
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int t = lt + 32 * r;
-            if (t0 + t < r1 && at < p_here) cp_async16(sm + L::kV + ((cc & 1) * kC + t) * 256 + 2 * at, src + t * v_row);
-        }
-    };
-    auto store_o = [&](int cc) {
-        const int t0 = r0 + cc * kC, at = lane * 4;
-        float *dst = a.y + (int64_t)t0 * v_row + (int64_t)h * P + p_base + at;
-        const float *src = reinterpret_cast<const float *>(sm + L::kO) + at;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int t = warp + 16 * r;
-            if (t0 + t < r1 && at < p_here) *reinterpret_cast<float4 *>(dst + t * v_row) = *reinterpret_cast<const float4 *>(src + t * 128);
-        }
-    };
-    if (nchunks > 0) {
-        load_rows(0);
-        load_v(0);
-    }
-    float s[32];  // S[p][32 grp ..]
-    const int64_t s_at = (((int64_t)b * H + h) * P + p) * kDk + 32 * grp;
-#pragma unroll
-    for (int j = 0; j < 32; j += 4) {
-        const float4 x = on && a.S0 ? *reinterpret_cast<const float4 *>(a.S0 + s_at + j) : make_float4(0.f, 0.f, 0.f, 0.f);
-        s[j] = x.x; s[j + 1] = x.y; s[j + 2] = x.z; s[j + 3] = x.w;
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tslot, base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-    if (tid == 0 && nchunks > 0) load_op(0);
-
     const uint32_t smem0 = smem_u32(sm);
-    bool failed = false;
-    // Operands written by this thread are in place; true when every wait so far has succeeded.
-    auto ready = [&]() {
-        tmem_st_wait();
-        fence_async_smem();
-        tc_fence_before();
-        failed = __syncthreads_or(failed);
-        tc_fence_after();
-        return !failed;
-    };
+    const int nchunks = (r1 - r0 + kC - 1) / kC;
+    const int64_t v_row = (int64_t)H * P;
+
+    // Wait for a barrier's phase; false, for every role, once any wait has run out.
     auto wait_for = [&](int which, int parity) {
-        __syncwarp();
-        if (!bar_wait(bar + which, parity)) failed = true;
+        if (!bar_try(bar + which, parity)) {
+            const long long t0 = clock64();
+            while (!bar_try(bar + which, parity))
+                if (*sfail || clock64() - t0 > kWaitCycles) {
+                    *sfail = 1;
+                    return false;
+                }
+        }
         tc_fence_after();
+        return true;
     };
-    // 16 fp32 as 8 columns of hi and of lo.
-    auto put16 = [&](const float *x, uint32_t hi_at, uint32_t lo_at) {
-        alignas(16) uint32_t hi[8], lo[8];
-        split8(x, *reinterpret_cast<uint4 *>(hi), *reinterpret_cast<uint4 *>(lo));
-        split8(x + 8, *reinterpret_cast<uint4 *>(hi + 4), *reinterpret_cast<uint4 *>(lo + 4));
-        tmem_st_u32(base + hi_at, hi);
-        tmem_st_u32(base + lo_at, lo);
+    // This warp's share is in place.
+    auto arrive = [&](int which) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar + which);
     };
-    float yq[16];
-    // O of chunk cc: 2^Lam (S q) + Z.
-    auto write_o = [&](int cc) {
-        wait_for(kBarZq, cc & 1);
-        float z[16];
-        tmem_ld16(base + kTmZq + 16 * grp, z);
-        const float4 *e = reinterpret_cast<const float4 *>(sm + L::kOp + (cc & 1) * L::kOpStep + 2 * kTile + 64 * grp);
-        float *dst = reinterpret_cast<float *>(sm + L::kO) + 16 * grp * 128 + row;
+
+    if (warp < kChainWarps) {
+        const int row = tid & 127, grp = tid >> 7, p = p_base + row;
+        const bool on = p < P;
+        const int64_t s_at = (((int64_t)b * H + h) * P + p) * kDk + 64 * grp;  // S[p][64 grp ..]
+        const uint32_t s_tm = base + kTmS + 64 * grp;
+#pragma unroll 1
+        for (int j0 = 0; j0 < 64; j0 += 32) {
+            float s[32];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float4 d = e[k];
+            for (int j = 0; j < 32; j += 4) {
+                const float4 x = on && a.S0 ? *reinterpret_cast<const float4 *>(a.S0 + s_at + j0 + j) : make_float4(0.f, 0.f, 0.f, 0.f);
+                s[j] = x.x; s[j + 1] = x.y; s[j + 2] = x.z; s[j + 3] = x.w;
+            }
+            tmem_st32(s_tm + j0, s);
+        }
+        // 16 fp32 as 8 columns of hi and of lo.
+        auto put16 = [&](const float *x, uint32_t hi_at, uint32_t lo_at) {
+            alignas(16) uint32_t hi[8], lo[8];
+            split8(x, *reinterpret_cast<uint4 *>(hi), *reinterpret_cast<uint4 *>(lo));
+            split8(x + 8, *reinterpret_cast<uint4 *>(hi + 4), *reinterpret_cast<uint4 *>(lo + 4));
+            tmem_st_u32(base + hi_at, hi);
+            tmem_st_u32(base + lo_at, lo);
+        };
+        bool ok = true;
+        for (int c = 0; c < nchunks; ++c) {
+            const int par = c & 1;
+            const float *dec = reinterpret_cast<const float *>(sm + L::kOp + par * L::kOpStep + 2 * kTile);
+            // S at the chunk's start as (hi, lo), then 2^{Lam_C} S.
+            // (It is read twice: 64 values held over the barrier would be spilled, and what is spilled comes back
+            // from L2, so little is left of L1.)
+            if (c > 0 && !(ok = wait_for(kBarS, par ^ 1))) break;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) dst[(4 * k + j) * 128] = fmaf((&d.x)[j], yq[4 * k + j], z[4 * k + j]);
+            for (int j0 = 0; j0 < 64; j0 += 32) {
+                float s[32];
+                tmem_ld32(s_tm + j0, s);
+                put16(s, kTmA + 32 * grp + j0 / 2, kTmA + 64 + 32 * grp + j0 / 2);
+                put16(s + 16, kTmA + 32 * grp + j0 / 2 + 8, kTmA + 64 + 32 * grp + j0 / 2 + 8);
+            }
+            tmem_st_wait();
+            arrive(kBarPutS);
+            if (!(ok = wait_for(kBarOp + par, (c >> 1) & 1))) break;
+            const float d = dec[kC - 1];
+#pragma unroll
+            for (int j0 = 0; j0 < 64; j0 += 32) {
+                float s[32];
+                tmem_ld32(s_tm + j0, s);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) s[j] *= d;
+                tmem_st32(s_tm + j0, s);
+            }
+            // R^T = V^T - Y^T 2^Lam (behind the prompt v and K are zero, and so is this).
+            if (!(ok = wait_for(kBarIn + par, (c >> 1) & 1))) break;
+            float x[32];
+            uint16_t v[32];
+            const uint16_t *vs = reinterpret_cast<const uint16_t *>(sm + L::kV + par * kC * 256) + 32 * grp * 128 + row;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = vs[j * 128];
+            if (!(ok = wait_for(kBarYk, par))) break;
+            tmem_ld32(base + kTmY + 32 * grp, x);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float4 e = reinterpret_cast<const float4 *>(dec + 32 * grp)[k];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[4 * k + j] = fmaf(-(&e.x)[j], x[4 * k + j], bf16_bits_to_float(v[4 * k + j]));
+            }
+            put16(x, kTmR + 16 * grp, kTmR + 32 + 16 * grp);
+            put16(x + 16, kTmR + 16 * grp + 8, kTmR + 32 + 16 * grp + 8);
+            tmem_st_wait();
+            arrive(kBarPutR);
+            if (!(ok = wait_for(kBarZk, par))) break;
+            tmem_ld32(base + kTmY + 32 * grp, x);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float4 w = reinterpret_cast<const float4 *>(dec + kC + 32 * grp)[k];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[4 * k + j] *= (&w.x)[j];
+            }
+            put16(x, kTmU + 16 * grp, kTmU + 32 + 16 * grp);
+            put16(x + 16, kTmU + 16 * grp + 8, kTmU + 32 + 16 * grp + 8);
+            tmem_st_wait();
+            arrive(kBarPutU);
         }
-    };
-    int c = 0;
-    for (; c < nchunks; ++c) {
-        const int par = c & 1;
-        // descriptors: K (Q's rows lie 8192 bytes on) along its columns, K along its tokens, the matrix
-        const uint32_t kq = sw128_desc_lo(smem0 + L::kKQ + par * 2 * kTile), kt = sw128_desc_lo(smem0 + L::kKQ + par * 2 * kTile, kTile);
-        const uint32_t op = sw128_desc_lo(smem0 + L::kOp + par * L::kOpStep);
-        const float *dec = reinterpret_cast<const float *>(sm + L::kOp + par * L::kOpStep + 2 * kTile);
-        // S at the chunk's start as (hi, lo).
-        if (c > 0) {
-            wait_for(kBarS, par ^ 1);
-            tmem_ld32(base + kTmS + 32 * grp, s);
+        if (ok && nchunks > 0) ok = wait_for(kBarS, (nchunks - 1) & 1);
+        if (ok)
+#pragma unroll 1
+            for (int j0 = 0; j0 < 64; j0 += 32) {
+                float s[32];
+                tmem_ld32(s_tm + j0, s);
+                if (on)
+#pragma unroll
+                    for (int j = 0; j < 32; j += 4)
+                        *reinterpret_cast<float4 *>(a.S_out + s_at + j0 + j) = make_float4(s[j], s[j + 1], s[j + 2], s[j + 3]);
+            }
+    } else if (warp < kFirstIn) {
+        // v and o meet global memory in runs of 16 bytes a lane along p: a warp's accesses of 2 and 4 bytes a lane
+        // took 1600 and 2500 cycles a chunk, a bulk copy a token about as long.
+        const int ot = tid - 32 * kChainWarps;  // = tensor-memory lane = state row
+        int meets = 0;
+        auto meet = [&] {
+            arrive(kBarOut);
+            return wait_for(kBarOut, meets++ & 1);
+        };
+        float *so = reinterpret_cast<float *>(sm + L::kO);
+        for (int c = 0; c < nchunks; ++c) {
+            if (!wait_for(kBarOp + (c & 1), (c >> 1) & 1) || !wait_for(kBarZq, c & 1)) break;
+            // O^T = 2^Lam (S q) + Z, to rows of p.
+            const float4 *e = reinterpret_cast<const float4 *>(sm + L::kOp + (c & 1) * L::kOpStep + 2 * kTile);
+#pragma unroll 1
+            for (int i0 = 0; i0 < kC; i0 += 32) {
+                float y[32], z[32];
+                tmem_ld32(base + kTmY + kC + i0, y);
+                tmem_ld32(base + kTmZq + i0, z);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float4 d = e[(i0 >> 2) + k];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) so[(i0 + 4 * k + j) * 128 + ot] = fmaf((&d.x)[j], y[4 * k + j], z[4 * k + j]);
+                }
+            }
+            arrive(kBarO);
+            if (!meet()) break;
+            const int t0 = r0 + c * kC, at = lane * 4;
+            float *dst = a.y + (int64_t)t0 * v_row + (int64_t)h * P + p_base + at;
+            if (at < p_here)
+#pragma unroll 4
+                for (int t = warp - kChainWarps; t < min(kC, r1 - t0); t += kOutWarps)
+                    *reinterpret_cast<float4 *>(dst + t * v_row) = *reinterpret_cast<const float4 *>(so + t * 128 + at);
+            if (!meet()) break;
         }
-        put16(s, kTmA + 16 * grp, kTmA + 64 + 16 * grp);
-        put16(s + 16, kTmA + 16 * grp + 8, kTmA + 64 + 16 * grp + 8);
+    } else if (warp < kIssuer) {
+        // 64 rows of 256 bytes a chunk for each warp (K, Q or v), 16 lanes a row, two rows a copy.  Rows behind the
+        // prompt and state rows behind P are zero.
+        const int what = warp - kFirstIn, ch = lane & 15, r = lane >> 4;
+        const int64_t step = 2 * (what == 2 ? v_row : (int64_t)H * kDk);
+        const __nv_bfloat16 *first = reinterpret_cast<const __nv_bfloat16 *>(what == 2 ? a.v : what ? a.q : a.k) +
+                                     (r0 + r) * (step / 2) + (what == 2 ? (int64_t)h * P + p_base : (int64_t)h * kDk) + 8 * ch;
+        const bool cols = what < 2 || 8 * ch < p_here;
+        // rows 8 apart lie 8 rows' bytes apart in either layout
+        uint32_t dst[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            dst[u] = what == 2 ? L::kV + 256 * (2 * u + r) + 16 * ch : L::kKQ + what * kC * 128 + sw128_chunk(2 * u + r, ch, 128);
+        const uint32_t dst_step = what == 2 ? 2048 : 1024, dst_buf = what == 2 ? kC * 256 : 2 * kTile;
+        auto load = [&](int cc) {
+            const int n = cols ? r1 - (r0 + cc * kC) - r : 0;
+            const __nv_bfloat16 *src = first + cc * (kC / 2) * step;
+            uint8_t *to = sm + (cc & 1) * dst_buf;
+#pragma unroll
+            for (int i = 0; i < kC / 2; ++i) {
+                cp_async16_or_zero(to + dst[i & 3] + (i >> 2) * dst_step, 2 * i < n ? src : first, 2 * i < n);
+                src += step;
+            }
+        };
+        for (int c = 0; c < nchunks; ++c) {
+            if (c >= 2 && !wait_for(kBarZq, c & 1)) break;  // chunk c - 2's products are done
+            load(c);
+            if (c >= 2 && !wait_for(kBarO, c & 1)) break;   // and its decays read
+            if (warp == kFirstIn && lane == 0) {
+                uint64_t *br = bar + kBarOp + (c & 1);
+                mbar_arrive_expect_tx(br, kSlot);
+                bulk_g2s(sm + L::kOp + (c & 1) * L::kOpStep, a.ws + ((int64_t)(r0 / kC + b + c) * H + h) * kSlot, kSlot, br);
+            }
+            cp_async_wait_all();
+            fence_async_smem();
+            arrive(kBarIn + (c & 1));
+        }
         cp_async_wait_all();
-        if (!ready()) break;
-        if (warp == 0 && elect_one()) {  // Y^T = S [K; Q]^T, the K tokens first
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
+        if (*sfail && warp == kFirstIn)  // copies that may still be in flight
+            for (int i = 0; i < 4; ++i) bar_wait(bar + kBarOp + (i & 1), i >> 1);
+    } else {
+        const bool lead = elect_one();
+        for (int c = 0; c < nchunks; ++c) {
+            const int par = c & 1, use = (c >> 1) & 1;
+            // descriptors: K (Q's rows lie 8192 bytes on) along its columns, K along its tokens, the matrix
+            const uint32_t kq = sw128_desc_lo(smem0 + L::kKQ + par * 2 * kTile), kt = sw128_desc_lo(smem0 + L::kKQ + par * 2 * kTile, kTile);
+            const uint32_t op = sw128_desc_lo(smem0 + L::kOp + par * L::kOpStep);
+            auto y_products = [&](int q) {  // Y^T = S [K; Q]^T
 #pragma unroll
                 for (int hl = 0; hl < 2; ++hl)
 #pragma unroll
@@ -522,97 +639,53 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const GdnPreA
                         umma_bf16_ts(tmem + kTmY + q * kC, tmem + kTmA + 64 * hl + 8 * ks,
                                      sw128_desc_of(kq + (q * kC * 128 + (ks >> 2) * kTile + (ks & 3) * 32) / 16),
                                      idesc_bf16_f32(128, kC), hl > 0 || ks > 0);
-                if (q == 0) umma_commit(bar + kBarYk);
+            };
+            auto z_products = [&](uint32_t d, int q) {  // Z^T = R^T [T b; M T b]^T
+#pragma unroll
+                for (int pr = 0; pr < 3; ++pr)
+#pragma unroll
+                    for (int ks = 0; ks < kC / 16; ++ks)
+                        umma_bf16_ts(d, tmem + kTmR + (pr == 2 ? 32 : 0) + 8 * ks,
+                                     sw128_desc_of(op + (q * kC * 128 + (pr == 1 ? kTile : 0) + ks * 32) / 16),
+                                     idesc_bf16_f32(128, kC), pr > 0 || ks > 0);
+            };
+            if (!wait_for(kBarIn + par, use) || !wait_for(kBarPutS, par)) break;
+            if (lead) {
+                y_products(0);
+                umma_commit(bar + kBarYk);
             }
+            if (c > 0 && !wait_for(kBarO, par ^ 1)) break;
+            if (lead) y_products(1);
+            if (!wait_for(kBarOp + par, use) || !wait_for(kBarPutR, par)) break;
+            if (lead) {
+                z_products(tmem + kTmY, 0);
+                umma_commit(bar + kBarZk);
+            }
+            if (!wait_for(kBarPutU, par)) break;
+            if (lead) {
+#pragma unroll
+                for (int hl = 0; hl < 2; ++hl)  // S += (w U)^T K
+#pragma unroll
+                    for (int ks = 0; ks < kC / 16; ++ks)
+                        umma_bf16_ts(tmem + kTmS, tmem + kTmU + 32 * hl + 8 * ks, sw128_desc_of(kt + ks * 2048 / 16),
+                                     idesc_bf16_f32_mn(128, kDk, false, true), true);
+                umma_commit(bar + kBarS);
+                z_products(tmem + kTmZq, 1);
+            }
+            // The next chunk's rows are there, so that every input warp has seen the phase of kBarZq before this
+            // one: no phase of it passes while someone waits for the one before.
+            if (c + 1 < nchunks && !wait_for(kBarIn + (par ^ 1), ((c + 1) >> 1) & 1)) break;
+            if (lead) umma_commit(bar + kBarZq);
         }
-        if (c > 0) write_o(c - 1);
-        wait_for(kBarOp + par, (c >> 1) & 1);
-        {  // 2^{Lam_C} S back into tensor memory
-            const float d = dec[kC - 1];
-#pragma unroll
-            for (int j = 0; j < 32; ++j) s[j] *= d;
-            tmem_st32(base + kTmS + 32 * grp, s);
+        if (*sfail) {  // products that may still run
+            if (lead) umma_commit(bar + kBarEnd);
+            __syncwarp();
+            bar_wait(bar + kBarEnd, 0);
         }
-        if (c + 1 < nchunks) {
-            load_rows(c + 1);
-            load_v(c + 1);
-        }
-        wait_for(kBarYk, par);
-        // R^T = V^T - Y^T 2^Lam; what lies behind the prompt is 0.
-        float x[16];
-        tmem_ld16(base + kTmY + 16 * grp, x);
-        const uint16_t *v = reinterpret_cast<const uint16_t *>(sm + L::kV + par * kC * 256) + 16 * grp * 128 + row;
-        const int live = on ? r1 - (r0 + c * kC) - 16 * grp : 0;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float4 d = reinterpret_cast<const float4 *>(dec + 16 * grp)[k];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                x[4 * k + j] = 4 * k + j < live ? fmaf(-(&d.x)[j], x[4 * k + j], bf16_bits_to_float(v[(4 * k + j) * 128])) : 0.f;
-        }
-        put16(x, kTmR + 8 * grp, kTmR + 32 + 8 * grp);
-        if (!ready()) break;
-        if (warp == 0 && elect_one()) {  // Z^T = R^T (T b)^T
-#pragma unroll
-            for (int pr = 0; pr < 3; ++pr)
-#pragma unroll
-                for (int ks = 0; ks < kC / 16; ++ks)
-                    umma_bf16_ts(tmem + kTmY, tmem + kTmR + (pr == 2 ? 32 : 0) + 8 * ks,
-                                 sw128_desc_of(op + ((pr == 1 ? kTile : 0) + ks * 32) / 16), idesc_bf16_f32(128, kC),
-                                 pr > 0 || ks > 0);
-            umma_commit(bar + kBarZk);
-            if (c + 1 < nchunks) load_op(c + 1);  // every thread has read the decays of chunk c - 1
-        }
-        if (c > 0) store_o(c - 1);
-        wait_for(kBarZk, par);
-        tmem_ld16(base + kTmY + 16 * grp, x);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float4 w = reinterpret_cast<const float4 *>(dec + kC + 16 * grp)[k];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) x[4 * k + j] *= (&w.x)[j];
-        }
-        put16(x, kTmU + 8 * grp, kTmU + 32 + 8 * grp);
-        tmem_ld16(base + kTmY + kC + 16 * grp, yq);
-        if (!ready()) break;
-        if (warp == 0 && elect_one()) {
-#pragma unroll
-            for (int hl = 0; hl < 2; ++hl)  // S += (w U)^T K
-#pragma unroll
-                for (int ks = 0; ks < kC / 16; ++ks)
-                    umma_bf16_ts(tmem + kTmS, tmem + kTmU + 32 * hl + 8 * ks, sw128_desc_of(kt + ks * 2048 / 16),
-                                 idesc_bf16_f32_mn(128, kDk, false, true), true);
-            umma_commit(bar + kBarS);
-#pragma unroll
-            for (int pr = 0; pr < 3; ++pr)  // Z^T of the Q tokens = R^T (M T b)^T
-#pragma unroll
-                for (int ks = 0; ks < kC / 16; ++ks)
-                    umma_bf16_ts(tmem + kTmZq, tmem + kTmR + (pr == 2 ? 32 : 0) + 8 * ks,
-                                 sw128_desc_of(op + (kC * 128 + (pr == 1 ? kTile : 0) + ks * 32) / 16), idesc_bf16_f32(128, kC),
-                                 pr > 0 || ks > 0);
-            umma_commit(bar + kBarZq);
-        }
-    }
-    if (!failed && nchunks > 0) {
-        wait_for(kBarS, (nchunks - 1) & 1);
-        write_o(nchunks - 1);
-        tmem_ld32(base + kTmS + 32 * grp, s);
-    }
-    cp_async_wait_all();
-    failed = __syncthreads_or(failed);
-    if (!failed && nchunks > 0) store_o(nchunks - 1);
-    if (failed) {
-        if (tid == 0) {
-            for (int i = 0; i < 2; ++i) bar_wait(bar + kBarOp + i, 0), bar_wait(bar + kBarOp + i, 1);  // copies still in flight
-            report_opt(a.err, DEV_PIPE_TIMEOUT, b, h, c);
-        }
-    } else if (on) {
-#pragma unroll
-        for (int j = 0; j < 32; j += 4)
-            *reinterpret_cast<float4 *>(a.S_out + s_at + j) = make_float4(s[j], s[j + 1], s[j + 2], s[j + 3]);
     }
     tc_fence_before();
     __syncthreads();
+    if (*sfail && tid == 0) report_opt(a.err, DEV_PIPE_TIMEOUT, b, h, 0);
     if (warp == 0) tmem_dealloc(tmem, 512);
 }
 

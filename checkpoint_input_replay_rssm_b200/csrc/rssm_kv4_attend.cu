@@ -114,12 +114,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ void cp_async16_or_zero(void *dst, const void *src, bool live) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
-                 "r"(live ? 16 : 0)
-                 : "memory");
-}
-
 // A row's power-of-two scale: the largest magnitude goes to [2^9, 2^10).
 __device__ __forceinline__ int row_exponent(float top) {
     const int e = (int)(__float_as_uint(top) >> 23);  // top >= 0

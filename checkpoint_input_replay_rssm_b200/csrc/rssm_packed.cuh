@@ -20,6 +20,13 @@ __device__ __forceinline__ bool packed_rows(const int32_t *cu, int b, int rows, 
     return r0 >= 0 && r0 <= r1 && r1 <= rows;
 }
 
+// 16-byte global -> shared copy, or 16 zeros (src is then not read).
+__device__ __forceinline__ void cp_async16_or_zero(void *dst, const void *src, bool live) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
+                 "r"(live ? 16 : 0)
+                 : "memory");
+}
+
 static inline bool aligned16(const void *p) { return ((uintptr_t)p & 15) == 0; }
 
 }  // namespace rssm
