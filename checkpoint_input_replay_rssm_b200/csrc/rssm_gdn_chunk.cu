@@ -90,24 +90,27 @@ __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity) {
 
 // ---------------------------------------------------------------- chunk operands
 constexpr int kLd = 68;  // fp32 row of A and T: 16-byte aligned, rows 4 banks apart
+constexpr int kChunkThreads = 256;
 struct ChunkSmem {
     static constexpr int kKQ = 0;  // [K; Q] 128 x 128 bf16 in two column blocks; A and T afterwards
     static constexpr int kT = kKQ + 2 * kC * kLd * 4;
     static constexpr int kHi = (kT + 1023) / 1024 * 1024;
     static constexpr int kLo = kHi + kTile;
-    static constexpr int kLam = kLo + kTile;  // Lam hi, Lam lo, beta
-    static constexpr int kBar = kLam + 3 * kC * 4;
+    static constexpr int kLam = kLo + kTile;  // Lam hi, Lam lo, beta, 2^{Lam_ref - Lam}
+    static constexpr int kBar = kLam + 4 * kC * 4;
     static constexpr int kBytes = kBar + 32;
 };
 static_assert(2 * kC * kLd * 4 >= 2 * 128 * 128, "A and T overlay the K, Q tile");
 
-__global__ void __launch_bounds__(128, 3) gdn_chunk_kernel(const GdnPreArgs a) {
+// 64 rows and 64 columns of fp32 products per CTA, three CTAs to an SM; the parts between the two products are
+// fp32 work out of shared memory, which bounds it.
+__global__ void __launch_bounds__(kChunkThreads, 3) gdn_chunk_kernel(const GdnPreArgs a) {
     using L = ChunkSmem;
     extern __shared__ __align__(1024) uint8_t raw[];
     uint8_t *sm = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
     uint8_t *sKQ = sm + L::kKQ, *sHi = sm + L::kHi, *sLo = sm + L::kLo;
     float *sA = reinterpret_cast<float *>(sm + L::kKQ), *sT = sA + kC * kLd;
-    float *lamh = reinterpret_cast<float *>(sm + L::kLam), *laml = lamh + kC, *sbeta = laml + kC;
+    float *lamh = reinterpret_cast<float *>(sm + L::kLam), *laml = lamh + kC, *sbeta = laml + kC, *sg = sbeta + kC;
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + L::kBar);
     uint32_t *tslot = reinterpret_cast<uint32_t *>(bar + 1);
     int *sfound = reinterpret_cast<int *>(bar + 2);
@@ -125,6 +128,7 @@ __global__ void __launch_bounds__(128, 3) gdn_chunk_kernel(const GdnPreArgs a) {
             lo += last * step;
         }
         if (lane == 0) *sfound = lo;
+    } else if (warp == 1) {
         tmem_alloc(tslot, 128);
         if (lane == 0) {
             mbar_init(bar, 1);
@@ -143,14 +147,18 @@ __global__ void __launch_bounds__(128, 3) gdn_chunk_kernel(const GdnPreArgs a) {
     bool failed = false;
     if (work) {
         const int Lc = min(kC, r1 - t0);
-        // K and Q rows, 16 lanes a row; rows behind the prompt are zero.
-        for (int i = tid; i < 128 * 16; i += 128) {
-            const int row = i >> 4, ch = i & 15, t = row & 63;
-            uint8_t *dst = sKQ + sw128_chunk(row, ch, 128);
-            const uint8_t *src = reinterpret_cast<const uint8_t *>(row < kC ? a.k : a.q) +
-                                 (((int64_t)(t0 + t) * H + h) * kDk) * 2 + 16 * ch;
-            if (t < Lc) cp_async16(dst, src);
-            else *reinterpret_cast<uint4 *>(dst) = make_uint4(0, 0, 0, 0);
+        // K and Q rows, 16 lanes a row, 16 rows a round; rows behind the prompt are zero.
+        {
+            const int r = tid >> 4, ch = tid & 15;
+            const int64_t at = ((int64_t)(t0 + r) * H + h) * kDk + 8 * ch, step = 16 * (int64_t)H * kDk;
+            const __nv_bfloat16 *k = reinterpret_cast<const __nv_bfloat16 *>(a.k) + at, *q = reinterpret_cast<const __nv_bfloat16 *>(a.q) + at;
+            uint8_t *dst = sKQ + sw128_chunk(r, ch, 128);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const bool live = r + 16 * i < Lc;
+                cp_async16_or_zero(dst + 2048 * i, live ? k + i * step : a.k, live);
+                cp_async16_or_zero(dst + 2048 * (i + 4), live ? q + i * step : a.q, live);
+            }
         }
         cp_async_commit();
         if (warp == 0) {
@@ -173,54 +181,76 @@ __global__ void __launch_bounds__(128, 3) gdn_chunk_kernel(const GdnPreArgs a) {
                 const double u = __shfl_up_sync(0xffffffffu, x, o);
                 if (lane >= o) x += u;
             }
+            const double ref = __shfl_sync(0xffffffffu, x, lane | 7);  // the last token of this 16-token block
+            const double end = __shfl_sync(0xffffffffu, x, 31);
+            float *out = reinterpret_cast<float *>(a.ws + ((int64_t)slot * H + h) * kSlot + 2 * kTile);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const double s = e ? x : x - v[1];
-                lamh[2 * lane + e] = (float)s;
-                laml[2 * lane + e] = (float)(s - (double)(float)s);
-                sbeta[2 * lane + e] = be[e];
+                const int t = 2 * lane + e;
+                lamh[t] = (float)s;
+                laml[t] = (float)(s - (double)(float)s);
+                sbeta[t] = be[e];
+                sg[t] = exp2f((float)(ref - s));
+                out[t] = exp2f((float)s);  // decays that the scan wants
+                out[kC + t] = exp2f((float)(end - s));
             }
         }
         cp_async_wait_all();
         fence_async_smem();
         __syncthreads();
         // G = [K; Q] K^T
-        if (tid == 0) {
-            const uint32_t at = smem_u32(sKQ);
-            for (int ks = 0; ks < kDk / 16; ++ks)
-                umma_bf16(tmem, sw128_desc(at, 128, ks), sw128_desc(at, 128, ks), idesc_bf16_f32(128, kC), ks > 0);
+        if (warp == 0 && elect_one()) {
+            const uint32_t d = sw128_desc_lo(smem_u32(sKQ));
+#pragma unroll
+            for (int ks = 0; ks < kDk / 16; ++ks) {
+                const uint64_t kd = sw128_desc_of(d + ((ks >> 2) * kTile + (ks & 3) * 32) / 16);
+                umma_bf16(tmem, kd, kd, idesc_bf16_f32(128, kC), ks > 0);
+            }
             umma_commit(bar);
-        }
-        const int i = tid & 63;
-        const float li = lamh[i], ll = laml[i];
-        if (tid < kC) {  // decays that the scan wants
-            float *out = reinterpret_cast<float *>(a.ws + ((int64_t)slot * H + h) * kSlot + 2 * kTile);
-            out[i] = exp2f(li + ll);
-            out[kC + i] = exp2f((lamh[kC - 1] - li) + (laml[kC - 1] - ll));
         }
         __syncwarp();
         failed = !bar_wait(bar, 0);
         failed = __syncthreads_or(failed);
         tc_fence_after();
         if (!failed) {
-            // Row i of A (threads of K rows) or of M (Q rows): its lower triangle with decays.
-            const uint32_t base = tmem + ((uint32_t)(32 * warp) << 16);
-            const float bi = tid < kC ? sbeta[i] : 1.f;
-            const int lim = tid < kC ? i : i + 1;  // columns below lim are kept
-            const int warp_lim = 32 * (warp & 1) + 32;
-#pragma unroll 1
-            for (int j0 = 0; j0 < kC; j0 += 16) {
-                float gv[16];
-                if (j0 < warp_lim) {  // warp-uniform
-                    tmem_ld16(base + j0, gv);
+            // Row i of A (lanes of K rows) or of M (Q rows), 32 columns a thread: its lower triangle with decays.
+            // Left of the diagonal's 16-column block the decay is 2^{Lam_i - Lam_ref} 2^{Lam_ref - Lam_j}, ref the
+            // last token of j's block, so that neither exponent is positive where gates are at most 1.
+            const uint32_t base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+            const int row = tid & 127, i = row & 63, half = tid >> 7;
+            const bool is_k = row < kC;
+            const float li = lamh[i], ll = laml[i], bi = is_k ? sbeta[i] : 1.f;
+            const int lim = is_k ? i : i + 1;       // columns below lim are kept
+            const int last_blk = 2 * (warp & 1) + 1;  // of this warp's rows
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        gv[j] = j0 + j < lim ? bi * ex2((li - lamh[j0 + j]) + (ll - laml[j0 + j])) * gv[j] : 0.f;
+            for (int q = 0; q < 2; ++q) {
+                const int blk = 2 * half + q, j0 = 16 * blk;
+                float gv[16];
+                if (blk <= last_blk) {  // warp-uniform
+                    tmem_ld16(base + j0, gv);
+                    const float f = bi * ex2((li - lamh[j0 + 15]) + (ll - laml[j0 + 15]));
+                    const bool diag = (i >> 4) == blk;
+#pragma unroll
+                    for (int j = 0; j < 16; j += 4) {
+                        const float4 g4 = *reinterpret_cast<const float4 *>(sg + j0 + j);
+                        float w[4] = {f * g4.x, f * g4.y, f * g4.z, f * g4.w};
+                        if (diag) {
+                            const float4 h4 = *reinterpret_cast<const float4 *>(lamh + j0 + j);
+                            const float4 l4 = *reinterpret_cast<const float4 *>(laml + j0 + j);
+                            w[0] = bi * ex2((li - h4.x) + (ll - l4.x));
+                            w[1] = bi * ex2((li - h4.y) + (ll - l4.y));
+                            w[2] = bi * ex2((li - h4.z) + (ll - l4.z));
+                            w[3] = bi * ex2((li - h4.w) + (ll - l4.w));
+                        }
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) gv[j + e] = j0 + j + e < lim ? w[e] * gv[j + e] : 0.f;
+                    }
                 } else {
 #pragma unroll
                     for (int j = 0; j < 16; ++j) gv[j] = 0.f;
                 }
-                if (tid < kC) {
+                if (is_k) {
 #pragma unroll
                     for (int j = 0; j < 16; j += 4)
                         *reinterpret_cast<float4 *>(sA + i * kLd + j0 + j) = make_float4(gv[j], gv[j + 1], gv[j + 2], gv[j + 3]);
@@ -229,88 +259,101 @@ __global__ void __launch_bounds__(128, 3) gdn_chunk_kernel(const GdnPreArgs a) {
                     for (int k = 0; k < 2; ++k) {
                         uint4 hi, lo;
                         split8(gv + 8 * k, hi, lo);
-                        *reinterpret_cast<uint4 *>(sHi + sw128_chunk(tid, (j0 >> 3) + k, 128)) = hi;
-                        *reinterpret_cast<uint4 *>(sLo + sw128_chunk(tid, (j0 >> 3) + k, 128)) = lo;
+                        *reinterpret_cast<uint4 *>(sHi + sw128_chunk(row, 2 * blk + k, 128)) = hi;
+                        *reinterpret_cast<uint4 *>(sLo + sw128_chunk(row, 2 * blk + k, 128)) = lo;
                     }
                 }
             }
             __syncthreads();
-            // T, diagonal blocks: thread (block, column).  The other threads clear the blocks above them.
+            // T, diagonal blocks: thread (block, column).  Other threads clear the blocks above them.
             if (tid < kC) {
                 const int d0 = tid & ~15, j = tid & 15;
                 float x[16];
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
                     float s = r == j ? 1.f : 0.f;
+                    const float4 *ar = reinterpret_cast<const float4 *>(sA + (d0 + r) * kLd + d0);
 #pragma unroll
-                    for (int k = 0; k < r; ++k) s = fmaf(-sA[(d0 + r) * kLd + d0 + k], x[k], s);
+                    for (int k = 0; k < r; k += 4) {
+                        const float4 v = ar[k >> 2];  // 0 from the diagonal on
+                        s = fmaf(-v.x, x[k], s);
+                        if (k + 1 < r) s = fmaf(-v.y, x[k + 1], s);
+                        if (k + 2 < r) s = fmaf(-v.z, x[k + 2], s);
+                        if (k + 3 < r) s = fmaf(-v.w, x[k + 3], s);
+                    }
                     x[r] = s;
                     sT[(d0 + r) * kLd + d0 + j] = s;
                 }
-            } else {
+            } else if (tid < 2 * kC) {
                 const int r = (tid - kC) >> 1, col = ((tid - kC) & 1) * 8;  // 32 rows: 0-15 and 32-47
-                const int row = (r & 15) + 32 * (r >> 4);
+                const int zr = (r & 15) + 32 * (r >> 4);
 #pragma unroll
                 for (int e = 0; e < 8; e += 4)
-                    *reinterpret_cast<float4 *>(sT + row * kLd + 32 * (r >> 4) + 16 + col + e) = make_float4(0.f, 0.f, 0.f, 0.f);
+                    *reinterpret_cast<float4 *>(sT + zr * kLd + 32 * (r >> 4) + 16 + col + e) = make_float4(0.f, 0.f, 0.f, 0.f);
             }
             __syncthreads();
             // T_21 = -T_22 (A_21 T_11), the bracket kept above A's diagonal: blocks of 16, then of 32.
             {
-                const int d0 = 32 * (tid >> 6), r = (tid & 63) >> 2, c0 = (tid & 3) * 4;
+                const int d0 = 32 * (tid >> 7), r = (tid & 127) >> 3, c0 = (tid & 7) * 2;
 #pragma unroll
                 for (int pass = 0; pass < 2; ++pass) {
                     const float *lhs = (pass ? sT + (d0 + 16 + r) * kLd + d0 + 16 : sA + (d0 + 16 + r) * kLd + d0);
                     const float *rhs = (pass ? sA + d0 * kLd + d0 + 16 : sT + d0 * kLd + d0) + c0;
-                    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-                    for (int k = 0; k < 16; ++k) {
-                        const float x = lhs[k];
-                        const float4 y = *reinterpret_cast<const float4 *>(rhs + k * kLd);
-                        s.x = fmaf(x, y.x, s.x); s.y = fmaf(x, y.y, s.y); s.z = fmaf(x, y.z, s.z); s.w = fmaf(x, y.w, s.w);
+                    float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+                    for (int k = 0; k < 16; k += 4) {
+                        const float4 x = *reinterpret_cast<const float4 *>(lhs + k);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 y = *reinterpret_cast<const float2 *>(rhs + (k + e) * kLd);
+                            s.x = fmaf((&x.x)[e], y.x, s.x);
+                            s.y = fmaf((&x.x)[e], y.y, s.y);
+                        }
                     }
-                    if (pass) *reinterpret_cast<float4 *>(sT + (d0 + 16 + r) * kLd + d0 + c0) = make_float4(-s.x, -s.y, -s.z, -s.w);
-                    else *reinterpret_cast<float4 *>(sA + (d0 + r) * kLd + d0 + 16 + c0) = s;
+                    if (pass) *reinterpret_cast<float2 *>(sT + (d0 + 16 + r) * kLd + d0 + c0) = make_float2(-s.x, -s.y);
+                    else *reinterpret_cast<float2 *>(sA + (d0 + r) * kLd + d0 + 16 + c0) = s;
                     __syncthreads();
                 }
             }
             {
-                const int r = tid >> 2, c0 = (tid & 3) * 8;
+                // a warp has 4 columns, a lane a row: the right factor is the same address for all lanes
+                const int c0 = 4 * warp;
 #pragma unroll
                 for (int pass = 0; pass < 2; ++pass) {
-                    const float *lhs = pass ? sT + (32 + r) * kLd + 32 : sA + (32 + r) * kLd;
+                    const float *lhs = pass ? sT + (32 + lane) * kLd + 32 : sA + (32 + lane) * kLd;
                     const float *rhs = (pass ? sA + 32 : sT) + c0;
-                    float s[8] = {};
-#pragma unroll 4
-                    for (int k = 0; k < 32; ++k) {
-                        const float x = lhs[k];
+                    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int k = pass ? 0 : c0; k < 32; k += 4) {  // T_11 is lower triangular
+                        const float4 x = *reinterpret_cast<const float4 *>(lhs + k);
 #pragma unroll
-                        for (int e = 0; e < 8; e += 4) {
-                            const float4 y = *reinterpret_cast<const float4 *>(rhs + k * kLd + e);
-                            s[e] = fmaf(x, y.x, s[e]); s[e + 1] = fmaf(x, y.y, s[e + 1]);
-                            s[e + 2] = fmaf(x, y.z, s[e + 2]); s[e + 3] = fmaf(x, y.w, s[e + 3]);
+                        for (int e = 0; e < 4; ++e) {
+                            const float4 y = *reinterpret_cast<const float4 *>(rhs + (k + e) * kLd);
+                            const float xe = (&x.x)[e];
+                            s.x = fmaf(xe, y.x, s.x); s.y = fmaf(xe, y.y, s.y); s.z = fmaf(xe, y.z, s.z); s.w = fmaf(xe, y.w, s.w);
                         }
                     }
-                    float *dst = pass ? sT + (32 + r) * kLd + c0 : sA + r * kLd + 32 + c0;
-                    const float sg = pass ? -1.f : 1.f;
-#pragma unroll
-                    for (int e = 0; e < 8; e += 4)
-                        *reinterpret_cast<float4 *>(dst + e) = make_float4(sg * s[e], sg * s[e + 1], sg * s[e + 2], sg * s[e + 3]);
+                    if (pass) *reinterpret_cast<float4 *>(sT + (32 + lane) * kLd + c0) = make_float4(-s.x, -s.y, -s.z, -s.w);
+                    else *reinterpret_cast<float4 *>(sA + lane * kLd + 32 + c0) = s;
                     __syncthreads();
                 }
             }
             // T diag(beta) as rows 0 .. 63 of the operand.
             {
-                const int half = (tid >> 6) * 32;
-#pragma unroll 1
-                for (int j0 = half; j0 < half + 32; j0 += 8) {
+                const int ti = tid & 63, q0 = (tid >> 6) * 16;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
                     float v[8];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) v[j] = j0 + j <= i ? sT[i * kLd + j0 + j] * sbeta[j0 + j] : 0.f;
+                    for (int j = 0; j < 8; j += 4) {
+                        const float4 t4 = *reinterpret_cast<const float4 *>(sT + ti * kLd + q0 + 8 * k + j);
+                        const float4 b4 = *reinterpret_cast<const float4 *>(sbeta + q0 + 8 * k + j);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) v[j + e] = q0 + 8 * k + j + e <= ti ? (&t4.x)[e] * (&b4.x)[e] : 0.f;
+                    }
                     uint4 hi, lo;
                     split8(v, hi, lo);
-                    *reinterpret_cast<uint4 *>(sHi + sw128_chunk(i, j0 >> 3, 128)) = hi;
-                    *reinterpret_cast<uint4 *>(sLo + sw128_chunk(i, j0 >> 3, 128)) = lo;
+                    *reinterpret_cast<uint4 *>(sHi + sw128_chunk(ti, (q0 >> 3) + k, 128)) = hi;
+                    *reinterpret_cast<uint4 *>(sLo + sw128_chunk(ti, (q0 >> 3) + k, 128)) = lo;
                 }
             }
             fence_async_smem();
@@ -318,14 +361,14 @@ __global__ void __launch_bounds__(128, 3) gdn_chunk_kernel(const GdnPreArgs a) {
             __syncthreads();
             tc_fence_after();
             // M (T diag(beta)): rows 64 .. 127 of the operand times its rows 0 .. 63, read as K x N.
-            if (tid == 0) {
-                const uint32_t hi = smem_u32(sHi), lo = smem_u32(sLo);
-                for (int pr = 0; pr < 3; ++pr) {
-                    const uint32_t A = pr == 2 ? lo : hi, B = pr == 1 ? lo : hi;
+            if (warp == 0 && elect_one()) {
+                const uint32_t hi = sw128_desc_lo(smem_u32(sHi)), lo = hi + kTile / 16;
+#pragma unroll
+                for (int pr = 0; pr < 3; ++pr)
+#pragma unroll
                     for (int ks = 0; ks < kC / 16; ++ks)
-                        umma_bf16(tmem + kC, sw128_desc(A, 128, ks), sw128_mn_desc(B, 1024, ks),
+                        umma_bf16(tmem + kC, sw128_desc_of((pr == 2 ? lo : hi) + ks * 2), sw128_desc_of((pr == 1 ? lo : hi) + ks * 128),
                                   idesc_bf16_f32_mn(128, kC, false, true), pr > 0 || ks > 0);
-                }
                 umma_commit(bar);
             }
             __syncwarp();
@@ -333,17 +376,18 @@ __global__ void __launch_bounds__(128, 3) gdn_chunk_kernel(const GdnPreArgs a) {
             failed = __syncthreads_or(failed);
             tc_fence_after();
             if (!failed) {
-                if (warp >= 2) {
-#pragma unroll 1
-                    for (int j0 = 0; j0 < kC; j0 += 16) {
+                if ((warp & 3) >= 2) {
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const int j0 = 32 * half + 16 * q;
                         float v[16];
                         tmem_ld16(base + kC + j0, v);
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
                             uint4 hi, lo;
                             split8(v + 8 * k, hi, lo);
-                            *reinterpret_cast<uint4 *>(sHi + sw128_chunk(tid, (j0 >> 3) + k, 128)) = hi;
-                            *reinterpret_cast<uint4 *>(sLo + sw128_chunk(tid, (j0 >> 3) + k, 128)) = lo;
+                            *reinterpret_cast<uint4 *>(sHi + sw128_chunk(row, (j0 >> 3) + k, 128)) = hi;
+                            *reinterpret_cast<uint4 *>(sLo + sw128_chunk(row, (j0 >> 3) + k, 128)) = lo;
                         }
                     }
                 }
@@ -360,7 +404,7 @@ __global__ void __launch_bounds__(128, 3) gdn_chunk_kernel(const GdnPreArgs a) {
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 0) tmem_dealloc(tmem, 128);
+    if (warp == 1) tmem_dealloc(tmem, 128);
 }
 
 // ---------------------------------------------------------------- scan over the chunks
@@ -368,14 +412,15 @@ __global__ void __launch_bounds__(128, 3) gdn_chunk_kernel(const GdnPreArgs a) {
 // state, the products Y^T = S [K; Q]^T and Z^T = R^T [T b; M T b]^T, and the left operands, which live in tensor
 // memory too (bf16 pairs) and never pass through shared memory.  v and o are then read and written along p, whole
 // lines at a time.
-// Columns: S fp32 (128); Y^T (K tokens, Q tokens; Z^T of the K tokens takes the first's place); S hi and lo (128), whose
-// place (w U)^T hi and lo take; Z^T of the Q tokens (64); R^T hi and lo (64).
+// Columns: S fp32 (128); Y^T of the K tokens, whose place Z^T of the K tokens and then (w U)^T take (16 tokens of it as
+// 8 columns of hi and 8 of lo, which are the columns that the warps writing them have read); Y^T of the Q tokens; S hi
+// and lo (128); Z^T of the Q tokens (64); R^T hi and lo (64).
 // The chain from state to state is S -> Y_k -> R -> Z_k -> U -> S; what only the outputs need is issued behind it
 // and read while the next chunk's first product runs.
-constexpr uint32_t kTmS = 0, kTmY = 128, kTmA = 256, kTmU = 256, kTmZq = 384, kTmR = 448;
+constexpr uint32_t kTmS = 0, kTmY = 128, kTmA = 256, kTmZq = 384, kTmR = 448;
 //
 // Roles, each a set of warps, meeting on barriers in shared memory only:
-//   8 chain warps   S, R and U of every chunk as operands: 2 a lane quarter, 64 state columns or 32 tokens each
+//  16 chain warps   S, R and U of every chunk as operands: 4 a lane quarter, 32 state columns or 16 tokens each
 //   4 output warps  the finished chunk's O
 //   3 input warps   the next chunks' rows into shared memory
 //   1 issuing warp  the products
@@ -388,7 +433,7 @@ struct ScanSmem {
     static constexpr int kBar = kO + kC * 512;
     static constexpr int kBytes = kBar + 128;
 };
-constexpr int kChainWarps = 8, kOutWarps = 4, kInWarps = 3;
+constexpr int kChainWarps = 16, kOutWarps = 4, kInWarps = 3;
 constexpr int kFirstIn = kChainWarps + kOutWarps, kIssuer = kFirstIn + kInWarps;
 constexpr int kScanThreads = 32 * (kIssuer + 1);
 enum ScanBar {
@@ -458,17 +503,16 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const GdnPreA
     if (warp < kChainWarps) {
         const int row = tid & 127, grp = tid >> 7, p = p_base + row;
         const bool on = p < P;
-        const int64_t s_at = (((int64_t)b * H + h) * P + p) * kDk + 64 * grp;  // S[p][64 grp ..]
-        const uint32_t s_tm = base + kTmS + 64 * grp;
-#pragma unroll 1
-        for (int j0 = 0; j0 < 64; j0 += 32) {
+        const int64_t s_at = (((int64_t)b * H + h) * P + p) * kDk + 32 * grp;  // S[p][32 grp ..]
+        const uint32_t s_tm = base + kTmS + 32 * grp;
+        {
             float s[32];
 #pragma unroll
             for (int j = 0; j < 32; j += 4) {
-                const float4 x = on && a.S0 ? *reinterpret_cast<const float4 *>(a.S0 + s_at + j0 + j) : make_float4(0.f, 0.f, 0.f, 0.f);
+                const float4 x = on && a.S0 ? *reinterpret_cast<const float4 *>(a.S0 + s_at + j) : make_float4(0.f, 0.f, 0.f, 0.f);
                 s[j] = x.x; s[j + 1] = x.y; s[j + 2] = x.z; s[j + 3] = x.w;
             }
-            tmem_st32(s_tm + j0, s);
+            tmem_st32(s_tm, s);
         }
         // 16 fp32 as 8 columns of hi and of lo.
         auto put16 = [&](const float *x, uint32_t hi_at, uint32_t lo_at) {
@@ -483,71 +527,65 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const GdnPreA
             const int par = c & 1;
             const float *dec = reinterpret_cast<const float *>(sm + L::kOp + par * L::kOpStep + 2 * kTile);
             // S at the chunk's start as (hi, lo), then 2^{Lam_C} S.
-            // (It is read twice: 64 values held over the barrier would be spilled, and what is spilled comes back
-            // from L2, so little is left of L1.)
+            // (It is read twice: values held over the barrier would be spilled, and what is spilled comes back from
+            // L2, so little is left of L1.)
             if (c > 0 && !(ok = wait_for(kBarS, par ^ 1))) break;
-#pragma unroll
-            for (int j0 = 0; j0 < 64; j0 += 32) {
+            {
                 float s[32];
-                tmem_ld32(s_tm + j0, s);
-                put16(s, kTmA + 32 * grp + j0 / 2, kTmA + 64 + 32 * grp + j0 / 2);
-                put16(s + 16, kTmA + 32 * grp + j0 / 2 + 8, kTmA + 64 + 32 * grp + j0 / 2 + 8);
+                tmem_ld32(s_tm, s);
+                put16(s, kTmA + 16 * grp, kTmA + 64 + 16 * grp);
+                put16(s + 16, kTmA + 16 * grp + 8, kTmA + 64 + 16 * grp + 8);
             }
             tmem_st_wait();
             arrive(kBarPutS);
             if (!(ok = wait_for(kBarOp + par, (c >> 1) & 1))) break;
-            const float d = dec[kC - 1];
-#pragma unroll
-            for (int j0 = 0; j0 < 64; j0 += 32) {
+            {
                 float s[32];
-                tmem_ld32(s_tm + j0, s);
+                const float d = dec[kC - 1];
+                tmem_ld32(s_tm, s);
 #pragma unroll
                 for (int j = 0; j < 32; ++j) s[j] *= d;
-                tmem_st32(s_tm + j0, s);
+                tmem_st32(s_tm, s);
             }
             // R^T = V^T - Y^T 2^Lam (behind the prompt v and K are zero, and so is this).
             if (!(ok = wait_for(kBarIn + par, (c >> 1) & 1))) break;
-            float x[32];
-            uint16_t v[32];
-            const uint16_t *vs = reinterpret_cast<const uint16_t *>(sm + L::kV + par * kC * 256) + 32 * grp * 128 + row;
+            float x[16];
+            uint16_t v[16];
+            const uint16_t *vs = reinterpret_cast<const uint16_t *>(sm + L::kV + par * kC * 256) + 16 * grp * 128 + row;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = vs[j * 128];
+            for (int j = 0; j < 16; ++j) v[j] = vs[j * 128];
             if (!(ok = wait_for(kBarYk, par))) break;
-            tmem_ld32(base + kTmY + 32 * grp, x);
+            tmem_ld16(base + kTmY + 16 * grp, x);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const float4 e = reinterpret_cast<const float4 *>(dec + 32 * grp)[k];
+            for (int k = 0; k < 4; ++k) {
+                const float4 e = reinterpret_cast<const float4 *>(dec + 16 * grp)[k];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) x[4 * k + j] = fmaf(-(&e.x)[j], x[4 * k + j], bf16_bits_to_float(v[4 * k + j]));
             }
-            put16(x, kTmR + 16 * grp, kTmR + 32 + 16 * grp);
-            put16(x + 16, kTmR + 16 * grp + 8, kTmR + 32 + 16 * grp + 8);
+            put16(x, kTmR + 8 * grp, kTmR + 32 + 8 * grp);
             tmem_st_wait();
             arrive(kBarPutR);
             if (!(ok = wait_for(kBarZk, par))) break;
-            tmem_ld32(base + kTmY + 32 * grp, x);
+            tmem_ld16(base + kTmY + 16 * grp, x);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const float4 w = reinterpret_cast<const float4 *>(dec + kC + 32 * grp)[k];
+            for (int k = 0; k < 4; ++k) {
+                const float4 w = reinterpret_cast<const float4 *>(dec + kC + 16 * grp)[k];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) x[4 * k + j] *= (&w.x)[j];
             }
-            put16(x, kTmU + 16 * grp, kTmU + 32 + 16 * grp);
-            put16(x + 16, kTmU + 16 * grp + 8, kTmU + 32 + 16 * grp + 8);
+            put16(x, kTmY + 16 * grp, kTmY + 16 * grp + 8);
             tmem_st_wait();
             arrive(kBarPutU);
         }
         if (ok && nchunks > 0) ok = wait_for(kBarS, (nchunks - 1) & 1);
-        if (ok)
-#pragma unroll 1
-            for (int j0 = 0; j0 < 64; j0 += 32) {
-                float s[32];
-                tmem_ld32(s_tm + j0, s);
-                if (on)
+        if (ok) {
+            float s[32];
+            tmem_ld32(s_tm, s);
+            if (on)
 #pragma unroll
-                    for (int j = 0; j < 32; j += 4)
-                        *reinterpret_cast<float4 *>(a.S_out + s_at + j0 + j) = make_float4(s[j], s[j + 1], s[j + 2], s[j + 3]);
-            }
+                for (int j = 0; j < 32; j += 4)
+                    *reinterpret_cast<float4 *>(a.S_out + s_at + j) = make_float4(s[j], s[j + 1], s[j + 2], s[j + 3]);
+        }
     } else if (warp < kFirstIn) {
         // v and o meet global memory in runs of 16 bytes a lane along p: a warp's accesses of 2 and 4 bytes a lane
         // took 1600 and 2500 cycles a chunk, a bulk copy a token about as long.
@@ -563,12 +601,12 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const GdnPreA
             // O^T = 2^Lam (S q) + Z, to rows of p.
             const float4 *e = reinterpret_cast<const float4 *>(sm + L::kOp + (c & 1) * L::kOpStep + 2 * kTile);
 #pragma unroll 1
-            for (int i0 = 0; i0 < kC; i0 += 32) {
-                float y[32], z[32];
-                tmem_ld32(base + kTmY + kC + i0, y);
-                tmem_ld32(base + kTmZq + i0, z);
+            for (int i0 = 0; i0 < kC; i0 += 16) {
+                float y[16], z[16];
+                tmem_ld16(base + kTmY + kC + i0, y);
+                tmem_ld16(base + kTmZq + i0, z);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
+                for (int k = 0; k < 4; ++k) {
                     const float4 d = e[(i0 >> 2) + k];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) so[(i0 + 4 * k + j) * 128 + ot] = fmaf((&d.x)[j], y[4 * k + j], z[4 * k + j]);
@@ -654,20 +692,20 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const GdnPreA
                 y_products(0);
                 umma_commit(bar + kBarYk);
             }
-            if (c > 0 && !wait_for(kBarO, par ^ 1)) break;
-            if (lead) y_products(1);
             if (!wait_for(kBarOp + par, use) || !wait_for(kBarPutR, par)) break;
             if (lead) {
                 z_products(tmem + kTmY, 0);
                 umma_commit(bar + kBarZk);
             }
+            if (c > 0 && !wait_for(kBarO, par ^ 1)) break;
+            if (lead) y_products(1);
             if (!wait_for(kBarPutU, par)) break;
             if (lead) {
 #pragma unroll
                 for (int hl = 0; hl < 2; ++hl)  // S += (w U)^T K
 #pragma unroll
                     for (int ks = 0; ks < kC / 16; ++ks)
-                        umma_bf16_ts(tmem + kTmS, tmem + kTmU + 32 * hl + 8 * ks, sw128_desc_of(kt + ks * 2048 / 16),
+                        umma_bf16_ts(tmem + kTmS, tmem + kTmY + 16 * ks + 8 * hl, sw128_desc_of(kt + ks * 2048 / 16),
                                      idesc_bf16_f32_mn(128, kDk, false, true), true);
                 umma_commit(bar + kBarS);
                 z_products(tmem + kTmZq, 1);
@@ -700,7 +738,7 @@ cudaError_t gdn_chunk_launch(const GdnPreArgs &a, cudaStream_t st) {
     cudaError_t e = cudaFuncSetAttribute(gdn_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, s1);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(gdn_scan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, s2);
     if (e != cudaSuccess) return e;
-    gdn_chunk_kernel<<<dim3((unsigned)slots(a.B, a.tokens), a.H), 128, s1, st>>>(a);
+    gdn_chunk_kernel<<<dim3((unsigned)slots(a.B, a.tokens), a.H), kChunkThreads, s1, st>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     gdn_scan_kernel<<<dim3(a.H * ((a.P + 127) / 128), a.B), kScanThreads, s2, st>>>(a);
     return cudaGetLastError();
