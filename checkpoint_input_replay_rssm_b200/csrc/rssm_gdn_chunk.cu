@@ -92,24 +92,22 @@ __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity) {
 constexpr int kLd = 68;  // fp32 row of A and T: 16-byte aligned, rows 4 banks apart
 constexpr int kChunkThreads = 256;
 struct ChunkSmem {
-    static constexpr int kKQ = 0;  // [K; Q] 128 x 128 bf16 in two column blocks; A and T afterwards
-    static constexpr int kT = kKQ + 2 * kC * kLd * 4;
-    static constexpr int kHi = (kT + 1023) / 1024 * 1024;
-    static constexpr int kLo = kHi + kTile;
-    static constexpr int kLam = kLo + kTile;  // Lam hi, Lam lo, beta, 2^{Lam_ref - Lam}
+    static constexpr int kKQ = 0;  // [K; Q] 128 x 128 bf16 in two column blocks; the operand's hi and lo afterwards
+    static constexpr int kHi = kKQ, kLo = kHi + kTile;
+    static constexpr int kA = kLo + kTile;  // A, and T in its place
+    static constexpr int kLam = kA + kC * kLd * 4;  // Lam hi, Lam lo, beta, 2^{Lam_ref - Lam}
     static constexpr int kBar = kLam + 4 * kC * 4;
     static constexpr int kBytes = kBar + 32;
 };
-static_assert(2 * kC * kLd * 4 >= 2 * 128 * 128, "A and T overlay the K, Q tile");
 
-// 64 rows and 64 columns of fp32 products per CTA, three CTAs to an SM; the parts between the two products are
-// fp32 work out of shared memory, which bounds it.
-__global__ void __launch_bounds__(kChunkThreads, 3) gdn_chunk_kernel(const GdnPreArgs a) {
+// Between the two products the work is fp32 out of shared memory in short steps with barriers between them: four CTAs
+// to an SM fill each other's waits, for which T takes A's place and the operand that of K and Q.
+__global__ void __launch_bounds__(kChunkThreads, 4) gdn_chunk_kernel(const GdnPreArgs a) {
     using L = ChunkSmem;
     extern __shared__ __align__(1024) uint8_t raw[];
     uint8_t *sm = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
     uint8_t *sKQ = sm + L::kKQ, *sHi = sm + L::kHi, *sLo = sm + L::kLo;
-    float *sA = reinterpret_cast<float *>(sm + L::kKQ), *sT = sA + kC * kLd;
+    float *sA = reinterpret_cast<float *>(sm + L::kA);
     float *lamh = reinterpret_cast<float *>(sm + L::kLam), *laml = lamh + kC, *sbeta = laml + kC, *sg = sbeta + kC;
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + L::kBar);
     uint32_t *tslot = reinterpret_cast<uint32_t *>(bar + 1);
@@ -265,40 +263,38 @@ __global__ void __launch_bounds__(kChunkThreads, 3) gdn_chunk_kernel(const GdnPr
                 }
             }
             __syncthreads();
-            // T, diagonal blocks: thread (block, column).  Other threads clear the blocks above them.
-            if (tid < kC) {
-                const int d0 = tid & ~15, j = tid & 15;
+            // T, diagonal blocks: thread (block, column).
+            {
+                const int d0 = tid & 48, j = tid & 15;
                 float x[16];
+                if (tid < kC) {
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    float s = r == j ? 1.f : 0.f;
-                    const float4 *ar = reinterpret_cast<const float4 *>(sA + (d0 + r) * kLd + d0);
+                    for (int r = 0; r < 16; ++r) {
+                        float s = r == j ? 1.f : 0.f;
+                        const float4 *ar = reinterpret_cast<const float4 *>(sA + (d0 + r) * kLd + d0);
 #pragma unroll
-                    for (int k = 0; k < r; k += 4) {
-                        const float4 v = ar[k >> 2];  // 0 from the diagonal on
-                        s = fmaf(-v.x, x[k], s);
-                        if (k + 1 < r) s = fmaf(-v.y, x[k + 1], s);
-                        if (k + 2 < r) s = fmaf(-v.z, x[k + 2], s);
-                        if (k + 3 < r) s = fmaf(-v.w, x[k + 3], s);
+                        for (int k = 0; k < r; k += 4) {
+                            const float4 v = ar[k >> 2];
+                            s = fmaf(-v.x, x[k], s);
+                            if (k + 1 < r) s = fmaf(-v.y, x[k + 1], s);
+                            if (k + 2 < r) s = fmaf(-v.z, x[k + 2], s);
+                            if (k + 3 < r) s = fmaf(-v.w, x[k + 3], s);
+                        }
+                        x[r] = s;
                     }
-                    x[r] = s;
-                    sT[(d0 + r) * kLd + d0 + j] = s;
-                }
-            } else if (tid < 2 * kC) {
-                const int r = (tid - kC) >> 1, col = ((tid - kC) & 1) * 8;  // 32 rows: 0-15 and 32-47
-                const int zr = (r & 15) + 32 * (r >> 4);
+                    __syncwarp();  // the warp's two blocks have been read
 #pragma unroll
-                for (int e = 0; e < 8; e += 4)
-                    *reinterpret_cast<float4 *>(sT + zr * kLd + 32 * (r >> 4) + 16 + col + e) = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int r = 0; r < 16; ++r) sA[(d0 + r) * kLd + d0 + j] = x[r];
+                }
             }
             __syncthreads();
-            // T_21 = -T_22 (A_21 T_11), the bracket kept above A's diagonal: blocks of 16, then of 32.
+            // T_21 = -T_22 (A_21 T_11) in A_21's place, the bracket kept above the diagonal: blocks of 16, then of 32.
             {
                 const int d0 = 32 * (tid >> 7), r = (tid & 127) >> 3, c0 = (tid & 7) * 2;
 #pragma unroll
                 for (int pass = 0; pass < 2; ++pass) {
-                    const float *lhs = (pass ? sT + (d0 + 16 + r) * kLd + d0 + 16 : sA + (d0 + 16 + r) * kLd + d0);
-                    const float *rhs = (pass ? sA + d0 * kLd + d0 + 16 : sT + d0 * kLd + d0) + c0;
+                    const float *lhs = sA + (d0 + 16 + r) * kLd + d0 + (pass ? 16 : 0);
+                    const float *rhs = sA + d0 * kLd + d0 + (pass ? 16 : 0) + c0;
                     float2 s = make_float2(0.f, 0.f);
 #pragma unroll
                     for (int k = 0; k < 16; k += 4) {
@@ -310,21 +306,24 @@ __global__ void __launch_bounds__(kChunkThreads, 3) gdn_chunk_kernel(const GdnPr
                             s.y = fmaf((&x.x)[e], y.y, s.y);
                         }
                     }
-                    if (pass) *reinterpret_cast<float2 *>(sT + (d0 + 16 + r) * kLd + d0 + c0) = make_float2(-s.x, -s.y);
+                    if (pass) *reinterpret_cast<float2 *>(sA + (d0 + 16 + r) * kLd + d0 + c0) = make_float2(-s.x, -s.y);
                     else *reinterpret_cast<float2 *>(sA + (d0 + r) * kLd + d0 + 16 + c0) = s;
                     __syncthreads();
                 }
             }
             {
-                // a warp has 4 columns, a lane a row: the right factor is the same address for all lanes
+                // A warp has 4 columns, a lane a row: the right factor is the same address for all lanes.  Where T has
+                // zeros above its diagonal blocks the array has brackets: they are passed over (the first product
+                // starts at its columns' row, in the second the first 16 rows end at 16).
                 const int c0 = 4 * warp;
 #pragma unroll
                 for (int pass = 0; pass < 2; ++pass) {
-                    const float *lhs = pass ? sT + (32 + lane) * kLd + 32 : sA + (32 + lane) * kLd;
-                    const float *rhs = (pass ? sA + 32 : sT) + c0;
+                    const float *lhs = sA + (32 + lane) * kLd + (pass ? 32 : 0);
+                    const float *rhs = sA + (pass ? 32 : 0) + c0;
                     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-                    for (int k = pass ? 0 : c0; k < 32; k += 4) {  // T_11 is lower triangular
-                        const float4 x = *reinterpret_cast<const float4 *>(lhs + k);
+                    for (int k = pass ? 0 : c0; k < 32; k += 4) {
+                        float4 x = *reinterpret_cast<const float4 *>(lhs + k);
+                        if (pass && k >= 16 && lane < 16) x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const float4 y = *reinterpret_cast<const float4 *>(rhs + (k + e) * kLd);
@@ -332,7 +331,7 @@ __global__ void __launch_bounds__(kChunkThreads, 3) gdn_chunk_kernel(const GdnPr
                             s.x = fmaf(xe, y.x, s.x); s.y = fmaf(xe, y.y, s.y); s.z = fmaf(xe, y.z, s.z); s.w = fmaf(xe, y.w, s.w);
                         }
                     }
-                    if (pass) *reinterpret_cast<float4 *>(sT + (32 + lane) * kLd + c0) = make_float4(-s.x, -s.y, -s.z, -s.w);
+                    if (pass) *reinterpret_cast<float4 *>(sA + (32 + lane) * kLd + c0) = make_float4(-s.x, -s.y, -s.z, -s.w);
                     else *reinterpret_cast<float4 *>(sA + lane * kLd + 32 + c0) = s;
                     __syncthreads();
                 }
@@ -345,7 +344,7 @@ __global__ void __launch_bounds__(kChunkThreads, 3) gdn_chunk_kernel(const GdnPr
                     float v[8];
 #pragma unroll
                     for (int j = 0; j < 8; j += 4) {
-                        const float4 t4 = *reinterpret_cast<const float4 *>(sT + ti * kLd + q0 + 8 * k + j);
+                        const float4 t4 = *reinterpret_cast<const float4 *>(sA + ti * kLd + q0 + 8 * k + j);
                         const float4 b4 = *reinterpret_cast<const float4 *>(sbeta + q0 + 8 * k + j);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) v[j + e] = q0 + 8 * k + j + e <= ti ? (&t4.x)[e] * (&b4.x)[e] : 0.f;
@@ -396,7 +395,7 @@ __global__ void __launch_bounds__(kChunkThreads, 3) gdn_chunk_kernel(const GdnPr
                 if (tid == 0) {
                     bulk_s2g(a.ws + ((int64_t)slot * H + h) * kSlot, sHi, 2 * kTile);
                     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-                    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+                    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
                 }
             }
         }
@@ -431,7 +430,7 @@ struct ScanSmem {
     static constexpr int kV = kOp + 2 * kOpStep;      // v [64 tokens][128 p] bf16, two buffers
     static constexpr int kO = kV + 2 * kC * 256;      // o [64 tokens][128 p] fp32
     static constexpr int kBar = kO + kC * 512;
-    static constexpr int kBytes = kBar + 128;
+    static constexpr int kBytes = kBar + 144;
 };
 constexpr int kChainWarps = 16, kOutWarps = 4, kInWarps = 3;
 constexpr int kFirstIn = kChainWarps + kOutWarps, kIssuer = kFirstIn + kInWarps;
@@ -443,7 +442,8 @@ enum ScanBar {
     kBarO,                          // Y and Z of the Q tokens and the decays read (every output warp arrives)
     kBarIn,                         // a chunk's K, Q and v rows in shared memory, per buffer (every input warp arrives)
     kBarOp = kBarIn + 2,            // a chunk's matrix and decays, per buffer
-    kBarEnd = kBarOp + 2,           // everything issued, after a failure
+    kBarEnd = kBarOp + 2,           // the state's way out (every chain warp arrives)
+    kBarDrain,                      // everything issued, after a failure
     kBarN
 };
 
@@ -466,7 +466,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const GdnPreA
     if (warp == 0) tmem_alloc(tslot, 512);
     if (tid == 0) {
         for (int i = 0; i < kBarN; ++i)
-            mbar_init(bar + i, i >= kBarPutS && i <= kBarPutU ? kChainWarps
+            mbar_init(bar + i, (i >= kBarPutS && i <= kBarPutU) || i == kBarEnd ? kChainWarps
                                : i == kBarOut || i == kBarO   ? kOutWarps
                                : i == kBarIn || i == kBarIn + 1 ? kInWarps : 1);
         *sfail = 0;
@@ -501,18 +501,33 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const GdnPreA
     };
 
     if (warp < kChainWarps) {
-        const int row = tid & 127, grp = tid >> 7, p = p_base + row;
-        const bool on = p < P;
-        const int64_t s_at = (((int64_t)b * H + h) * P + p) * kDk + 32 * grp;  // S[p][32 grp ..]
-        const uint32_t s_tm = base + kTmS + 32 * grp;
-        {
-            float s[32];
+        const int row = tid & 127, grp = tid >> 7;
+        const uint32_t s_tm = base + kTmS + 32 * grp;  // S[p][32 grp ..]
+        // The state in and out passes through shared memory: 32 lanes of a row each read whole lines, a lane a row
+        // 32 of them for 16 bytes each.  Chunks of 16 bytes are exchanged by row so that neither side has conflicts.
+        auto chain_meet = [] { asm volatile("bar.sync 2, %0;" ::"n"(32 * kChainWarps) : "memory"); };
+        float *st = reinterpret_cast<float *>(sm + L::kO);  // [128 p][64 n] at a time
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
 #pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-                const float4 x = on && a.S0 ? *reinterpret_cast<const float4 *>(a.S0 + s_at + j) : make_float4(0.f, 0.f, 0.f, 0.f);
-                s[j] = x.x; s[j + 1] = x.y; s[j + 2] = x.z; s[j + 3] = x.w;
+            for (int r = 0; r < 4; ++r) {
+                const int pr = (tid >> 4) + 32 * r, ch = tid & 15;
+                const bool live = a.S0 && pr < p_here;
+                const float *src = a.S0 + ((((int64_t)b * H + h) * P + p_base + pr) * kDk + 64 * half + 4 * ch);
+                cp_async16_or_zero(st + pr * 64 + 4 * (ch ^ (pr & 7)), live ? src : a.y, live);
             }
-            tmem_st32(s_tm, s);
+            cp_async_wait_all();
+            chain_meet();
+            if ((grp >> 1) == half) {
+                float s[32];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float4 x = *reinterpret_cast<const float4 *>(st + row * 64 + 4 * ((8 * (grp & 1) + j) ^ (row & 7)));
+                    s[4 * j] = x.x; s[4 * j + 1] = x.y; s[4 * j + 2] = x.z; s[4 * j + 3] = x.w;
+                }
+                tmem_st32(s_tm, s);
+            }
+            chain_meet();
         }
         // 16 fp32 as 8 columns of hi and of lo.
         auto put16 = [&](const float *x, uint32_t hi_at, uint32_t lo_at) {
@@ -577,14 +592,25 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const GdnPreA
             tmem_st_wait();
             arrive(kBarPutU);
         }
-        if (ok && nchunks > 0) ok = wait_for(kBarS, (nchunks - 1) & 1);
+        // All products are done, so that K's and Q's place is free.
+        if (ok && nchunks > 0) ok = wait_for(kBarS, (nchunks - 1) & 1) && wait_for(kBarZq, (nchunks - 1) & 1);
         if (ok) {
             float s[32];
             tmem_ld32(s_tm, s);
-            if (on)
+            st = reinterpret_cast<float *>(sm + L::kKQ);  // [128 p][128 n]
 #pragma unroll
-                for (int j = 0; j < 32; j += 4)
-                    *reinterpret_cast<float4 *>(a.S_out + s_at + j) = make_float4(s[j], s[j + 1], s[j + 2], s[j + 3]);
+            for (int j = 0; j < 8; ++j)
+                *reinterpret_cast<float4 *>(st + row * 128 + 4 * ((8 * grp + j) ^ (row & 7))) = make_float4(s[4 * j], s[4 * j + 1], s[4 * j + 2], s[4 * j + 3]);
+            arrive(kBarEnd);
+            ok = wait_for(kBarEnd, 0);
+        }
+        if (ok) {
+            float *dst = a.S_out + (((int64_t)b * H + h) * P + p_base) * kDk + 4 * lane;
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                const int pr = warp + 16 * r;
+                if (pr < p_here) *reinterpret_cast<float4 *>(dst + pr * kDk) = *reinterpret_cast<const float4 *>(st + pr * 128 + 4 * (lane ^ (pr & 7)));
+            }
         }
     } else if (warp < kFirstIn) {
         // v and o meet global memory in runs of 16 bytes a lane along p: a warp's accesses of 2 and 4 bytes a lane
@@ -716,9 +742,9 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const GdnPreA
             if (lead) umma_commit(bar + kBarZq);
         }
         if (*sfail) {  // products that may still run
-            if (lead) umma_commit(bar + kBarEnd);
+            if (lead) umma_commit(bar + kBarDrain);
             __syncwarp();
-            bar_wait(bar + kBarEnd, 0);
+            bar_wait(bar + kBarDrain, 0);
         }
     }
     tc_fence_before();
