@@ -11,7 +11,9 @@ and out with plain bf16 GEMMs (torch.matmul) after an RMS normalisation of its
 input (pre-norm residual blocks, as in the hybrid models); the attention layer
 appends the token's key and value to a bf16 cache and attends over it with
 torch.nn.functional.scaled_dot_product_attention (grouped-query: the query heads
-of a key/value head stacked as its query rows; flash or memory-efficient kernel).  The Mamba-2
+of a key/value head stacked as its query rows; flash or memory-efficient kernel), or, with
+``kv_cache="fp4"``, keeps and reads its keys and values in the library's paged 4-bit cache
+(rssm_build_tables once a step, rssm_kv4_append and rssm_kv4_attend per layer).  The Mamba-2
 layer's short convolution and output gate are left out: they carry no decode
 state that the method changes.
 
@@ -49,16 +51,22 @@ class HybridStack:
     """``blocks`` x (``ssm_per_block`` Mamba-2 layers + 1 attention layer) on one GPU.
 
     ssm_mode: "replay" (checkpoint + read copy ``read_dtype`` + buffer) or "eager"
-    (fp32 state rewritten every token).  Weights, initial states and the cached
-    keys/values come from a seeded torch generator.
+    (fp32 state rewritten every token).  kv_cache: "bf16" (a dense cache, torch attention)
+    or "fp4" (the paged 4-bit cache and its attention, pages of ``page_size`` tokens).
+    Weights, initial states and the cached keys/values come from a seeded torch generator.
     """
 
+    KV_SCALE = 2.0 ** -4  # tensor scale of the 4-bit cache: block maxima around 1 lie mid-range of its e4m3 scales
+
     def __init__(self, shape: HybridShape, ssm_mode: str = "replay", read_dtype: str = "bf16", seed: int = 0,
-                 device="cuda", max_steps: int = 512):
+                 device="cuda", max_steps: int = 512, kv_cache: str = "bf16", page_size: int = 64):
         import torch
 
         from . import rssm
 
+        if kv_cache not in ("bf16", "fp4"):
+            raise ValueError(f"kv_cache must be 'bf16' or 'fp4', got {kv_cache!r}")
+        self.rssm, self.kv_cache, self.page_size = rssm, kv_cache, page_size
         self.s = s = shape
         self.torch = torch
         self.device = torch.device(device)
@@ -100,10 +108,42 @@ class HybridStack:
         # milliseconds of host time per new length).
         from torch.nn.attention import SDPBackend, sdpa_kernel
 
+        if kv_cache == "fp4":
+            self._to_fp4(max_steps)
+
         self._sdpa_backends = lambda: sdpa_kernel([SDPBackend.FLASH_ATTENTION, SDPBackend.EFFICIENT_ATTENTION])
         self.pos = s.context  # next cache position
         self.cap = s.context + max_steps
         self.ssm_events = None  # a list here records CUDA events around every SSM decode call
+
+    def _to_fp4(self, max_steps):
+        """Move every attention layer's cached tokens into a paged 4-bit cache; the layers share one block table."""
+        torch, s, rssm, ps = self.torch, self.s, self.rssm, self.page_size
+        i32 = dict(dtype=torch.int32, device=self.device)
+        width = -(-(s.context + max_steps) // ps)
+        self.block_table = torch.full((s.batch, width), -1, **i32)
+        self.free_pages = torch.arange(s.batch * width, **i32)
+        self.free_head, self.cached_len = torch.zeros(1, **i32), torch.zeros(s.batch, **i32)
+        self.one_new = torch.ones(s.batch, **i32)
+        self.kv_err = torch.zeros(4, **i32)
+        slots = None
+        if s.context:
+            slots = self._tables(torch.full((s.batch,), s.context, **i32), s.batch * s.context)[2]
+            self._advance()
+        for kind, p in self.layers:
+            if kind == "attn":
+                k, v = (p.pop(n)[:, :, :s.context].transpose(1, 2).reshape(-1, s.n_kv_heads, s.head_dim) for n in "kv")
+                p["cache"] = rssm.kv4_cache(s.batch * width, s.n_kv_heads, ps, s.head_dim, device=self.device)
+                if slots is not None:
+                    rssm.kv4_append(k, v, slots, p["cache"], k_scale=self.KV_SCALE, v_scale=self.KV_SCALE, err=self.kv_err)
+
+    def _tables(self, new_len, max_tokens):
+        self.tables = self.rssm.build_tables(self.cached_len, new_len, self.free_pages, self.free_head, self.block_table,
+                                             self.page_size, max_tokens, err=self.kv_err)
+        return self.tables
+
+    def _advance(self):
+        self.cached_len, self.free_head = self.tables[1], self.tables[4]
 
     def _norm(self, x):
         xf = x.float()
@@ -133,6 +173,14 @@ class HybridStack:
     def _attn(self, x, p):
         torch, s = self.torch, self.s
         xn = self._norm(x)
+        if self.kv_cache == "fp4":
+            cu, seq_len, slots, _, _ = self.tables
+            heads = lambda w, n: (xn @ w).reshape(s.batch, n, s.head_dim)  # noqa: E731
+            sc = dict(k_scale=self.KV_SCALE, v_scale=self.KV_SCALE, err=self.kv_err)
+            self.rssm.kv4_append(heads(p["wk"], s.n_kv_heads), heads(p["wv"], s.n_kv_heads), slots, p["cache"], **sc)
+            o = self.rssm.kv4_attend(heads(p["wq"], s.n_q_heads), p["cache"], self.block_table, seq_len, cu, 1,
+                                     max_seq=self.cap, **sc)
+            return x + o.reshape(s.batch, s.n_q_heads * s.head_dim) @ p["wo"]
         # One decode token: the query heads that share a key/value head attend to
         # the same cache, so they are stacked as that head's query rows
         # ([batch, kv heads, query heads per kv head, head_dim]); query head j
@@ -150,9 +198,13 @@ class HybridStack:
         """One decode token for every sequence: hidden state x [batch, d_model] bf16 -> the next."""
         if self.pos >= self.cap:
             raise RuntimeError("the attention cache is full; build the stack with a larger max_steps")
+        if self.kv_cache == "fp4":
+            self._tables(self.one_new, self.s.batch)
         for kind, p in self.layers:
             x = self._ssm(x, p) if kind == "ssm" else self._attn(x, p)
         self.pos += 1
+        if self.kv_cache == "fp4":
+            self._advance()
         return x
 
     def ssm_layers(self):

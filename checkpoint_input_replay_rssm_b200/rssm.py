@@ -261,62 +261,68 @@ def prefill(x, dt, Bm, Cm, A, D, S0=None, dt_scales_input=False, y=None, S_out=N
 
 
 # ---------------------------------------------------------------- packed requests
-class _Call:
-    """Device and stream of one packed-request call: the tensors' device is current inside, and
-    what is allocated inside belongs to the stream that the kernels run on."""
+# These calls are a few microseconds of GPU work where they serve single tokens, so what surrounds a launch is kept short.
+class _OnStream:
+    """The tensors' device is current inside; with a stream given, what is allocated inside belongs to it and the
+    tensors used there are not handed out again before it is done with them."""
 
-    def __init__(self, device, stream, *inputs):
+    def __init__(self, idx, stream, tensors):
         import torch
 
-        self.torch, self.device, self.given = torch, device, stream
-        self.guard = torch.cuda.device(device) if torch.cuda.current_device() != device.index else None
-        self.inputs = inputs
+        if stream is not None and stream.device_index != idx:
+            raise ValueError(f"the stream is on cuda:{stream.device_index}, the tensors on cuda:{idx}")
+        self.ctx = [torch.cuda.device(idx)] + ([torch.cuda.stream(stream)] if stream is not None else [])
+        if stream is not None and stream != torch.cuda.current_stream(idx):
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(stream)
 
     def __enter__(self):
-        torch = self.torch
-        if self.guard is not None:
-            self.guard.__enter__()
-        self.ctx = None
-        if self.given is not None:
-            if self.given.device != self.device:
-                if self.guard is not None:
-                    self.guard.__exit__(None, None, None)
-                raise ValueError(f"the stream is on {self.given.device}, the tensors on {self.device}")
-            if self.given != torch.cuda.current_stream(self.device):
-                # tensors of another stream must not be handed out again before this one is done with them
-                for t in self.inputs:
-                    if t is not None:
-                        t.record_stream(self.given)
-            self.ctx = torch.cuda.stream(self.given)
-            self.ctx.__enter__()
-        return (self.given or torch.cuda.current_stream(self.device)).cuda_stream
+        for c in self.ctx:
+            c.__enter__()
 
     def __exit__(self, *a):
-        if self.ctx is not None:
-            self.ctx.__exit__(*a)
-        if self.guard is not None:
-            self.guard.__exit__(*a)
-        return False
+        for c in reversed(self.ctx):
+            c.__exit__(*a)
 
 
-def _want(name, t, dtype, shape, device):
-    """Pointer of a dense CUDA tensor of the given dtype, shape (None: any size) and device."""
-    if t.dtype != dtype or not t.is_cuda or t.device != device or not t.is_contiguous() or t.dim() != len(shape) \
-            or any(w is not None and w != n for w, n in zip(shape, t.shape)):
-        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape "
-                         f"{tuple('*' if w is None else w for w in shape)} on {device}, got {t.dtype} "
-                         f"{tuple(t.shape)} on {t.device}")
+def _run(call, idx, stream, tensors):
+    """call(stream pointer) on the tensors' device, on ``stream`` or the device's current one."""
+    import torch
+
+    if stream is None and torch._C._cuda_getDevice() == idx:
+        return call(torch._C._cuda_getCurrentRawStream(idx))
+    with _OnStream(idx, stream, tensors):
+        return call(torch._C._cuda_getCurrentRawStream(idx))
+
+
+def _want(name, t, dtype, shape, idx):
+    """Pointer of a dense CUDA tensor of the given dtype, shape and device index."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != idx or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{idx}, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
-def _opt(name, t, dtype, shape, device):
-    return None if t is None else _want(name, t, dtype, shape, device)
+def _opt(name, t, dtype, shape, idx):
+    return None if t is None else _want(name, t, dtype, shape, idx)
 
 
-def _cuda_device(t, name):
+def _workspace(t, need, idx, device):
+    """(tensor, pointer, bytes) of the caller's workspace or of a new one."""
+    import torch
+
+    if t is None:
+        if not need:
+            return None, None, 0
+        t = torch.empty(need, dtype=torch.uint8, device=device)
+    return t, _want("workspace", t, torch.uint8, (t.numel(),), idx), t.numel()
+
+
+def _cuda_index(t, name):
     if not t.is_cuda:
         raise ValueError(f"{name}: expected a CUDA tensor, got one on {t.device}")
-    return t.device
+    return t.get_device()
 
 
 def _ok(st, what):
@@ -335,29 +341,30 @@ def gdn_prefill(q, k, v, alpha, beta, cu_seqlens, S0=None, y=None, S_out=None, w
     """
     import torch
 
-    dev = _cuda_device(q, "q")
+    dev = _cuda_index(q, "q")
     if q.dim() != 3 or v.dim() != 3 or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
         raise ValueError("expected q, k, v of shape [tokens, heads, dim] and cu_seqlens of [requests + 1]")
     T, H, N = q.shape
-    P, Bn = v.shape[2], cu_seqlens.shape[0] - 1
-    if q.dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError(f"q: expected bfloat16 or float32, got {q.dtype}")
-    f32, i32 = torch.float32, torch.int32
-    with _Call(dev, stream, q, k, v, alpha, beta, cu_seqlens, S0, y, S_out, workspace, err) as st:
-        y = torch.empty((T, H, P), dtype=f32, device=dev) if y is None else y
-        S_out = torch.empty((Bn, H, P, N), dtype=f32, device=dev) if S_out is None else S_out
-        cfg = rssm_gdn_prefill_config(Bn, H, P, N, RSSM_BF16 if q.dtype == torch.bfloat16 else RSSM_F32, T)
-        need = int(load().rssm_gdn_prefill_workspace_bytes(ctypes.byref(cfg)))
-        if need and workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        ins = rssm_inputs(q=_want("q", q, q.dtype, (T, H, N), dev), k=_want("k", k, q.dtype, (T, H, N), dev),
-                          v=_want("v", v, q.dtype, (T, H, P), dev), alpha=_want("alpha", alpha, f32, (T, H), dev),
+    P, Bn, dt, f32, i32 = v.shape[2], cu_seqlens.shape[0] - 1, q.dtype, torch.float32, torch.int32
+    if dt is not torch.bfloat16 and dt is not f32:
+        raise ValueError(f"q: expected bfloat16 or float32, got {dt}")
+
+    def call(st):
+        nonlocal y, S_out
+        y = torch.empty((T, H, P), dtype=f32, device=q.device) if y is None else y
+        S_out = torch.empty((Bn, H, P, N), dtype=f32, device=q.device) if S_out is None else S_out
+        lib = load()
+        cfg = ctypes.byref(rssm_gdn_prefill_config(Bn, H, P, N, RSSM_BF16 if dt is torch.bfloat16 else RSSM_F32, T))
+        _, ws, nb = _workspace(workspace, lib.rssm_gdn_prefill_workspace_bytes(cfg), dev, q.device)
+        ins = rssm_inputs(q=_want("q", q, dt, (T, H, N), dev), k=_want("k", k, dt, (T, H, N), dev),
+                          v=_want("v", v, dt, (T, H, P), dev), alpha=_want("alpha", alpha, f32, (T, H), dev),
                           beta=_want("beta", beta, f32, (T, H), dev))
-        _ok(load().rssm_gdn_prefill(
-            ctypes.byref(cfg), _opt("S0", S0, f32, (Bn, H, P, N), dev), ctypes.byref(ins),
+        return lib.rssm_gdn_prefill(
+            cfg, _opt("S0", S0, f32, (Bn, H, P, N), dev), ctypes.byref(ins),
             _want("cu_seqlens", cu_seqlens, i32, (Bn + 1,), dev), _want("y", y, f32, (T, H, P), dev),
-            _want("S_out", S_out, f32, (Bn, H, P, N), dev), _opt("workspace", workspace, torch.uint8, (None,), dev),
-            0 if workspace is None else workspace.shape[0], _opt("err", err, i32, (4,), dev), st), "rssm_gdn_prefill")
+            _want("S_out", S_out, f32, (Bn, H, P, N), dev), ws, nb, _opt("err", err, i32, (4,), dev), st)
+
+    _ok(_run(call, dev, stream, (q, k, v, alpha, beta, cu_seqlens, S0, y, S_out, workspace, err)), "rssm_gdn_prefill")
     return y, S_out
 
 
@@ -368,25 +375,26 @@ def build_tables(cached_len, new_len, free_pages, free_head, block_table, page_s
     slot_map [max_tokens], position [max_tokens], next_free [1])."""
     import torch
 
-    dev, i32 = _cuda_device(cached_len, "cached_len"), torch.int32
+    dev, i32 = _cuda_index(cached_len, "cached_len"), torch.int32
     if cached_len.dim() != 1 or block_table.dim() != 2 or free_pages.dim() != 1:
         raise ValueError("expected cached_len [requests], block_table [requests, pages] and free_pages [pages]")
-    Bn, width = cached_len.shape[0], block_table.shape[1]
-    with _Call(dev, stream, cached_len, new_len, free_pages, free_head, block_table, err) as st:
-        # one allocation for the five results, each on a 16-byte boundary
-        sizes = (Bn + 1, Bn, max_tokens, max_tokens, 1)
-        at = [0]
-        for n in sizes:
-            at.append(at[-1] + (max(n, 1) + 3 & ~3))
-        buf = torch.empty(at[-1], dtype=i32, device=dev)
-        out = tuple(buf[a:a + n] for a, n in zip(at, sizes))
-        base = buf.data_ptr()
+    Bn, width = block_table.shape
+    if max_tokens < 1:
+        raise ValueError(f"max_tokens: expected at least 1, got {max_tokens}")
+    sizes, out = (Bn + 1, Bn, max_tokens, max_tokens, 1), None
+
+    def call(st):
+        nonlocal out
+        out = torch.empty(2 * Bn + 2 * max_tokens + 2, dtype=i32, device=cached_len.device).split_with_sizes(sizes)  # one allocation
+        base = out[0].data_ptr()
         cfg = rssm_tables_config(Bn, page_size, width, free_pages.shape[0], max_tokens)
-        _ok(load().rssm_build_tables(
-            ctypes.byref(cfg), _want("cached_len", cached_len, i32, (Bn,), dev),
-            _want("new_len", new_len, i32, (Bn,), dev), _want("free_pages", free_pages, i32, (None,), dev),
-            _want("free_head", free_head, i32, (1,), dev), _want("block_table", block_table, i32, (Bn, width), dev),
-            *(base + 4 * a for a in at[:5]), _opt("err", err, i32, (4,), dev), st), "rssm_build_tables")
+        return load().rssm_build_tables(
+            ctypes.byref(cfg), _want("cached_len", cached_len, i32, (Bn,), dev), _want("new_len", new_len, i32, (Bn,), dev),
+            _want("free_pages", free_pages, i32, (free_pages.shape[0],), dev), _want("free_head", free_head, i32, (1,), dev),
+            _want("block_table", block_table, i32, (Bn, width), dev), base, base + 4 * (Bn + 1), base + 4 * (2 * Bn + 1),
+            base + 4 * (2 * Bn + 1 + max_tokens), base + 4 * (2 * Bn + 1 + 2 * max_tokens), _opt("err", err, i32, (4,), dev), st)
+
+    _ok(_run(call, dev, stream, (cached_len, new_len, free_pages, free_head, block_table, err)), "rssm_build_tables")
     return out
 
 
@@ -420,14 +428,17 @@ def kv4_append(k, v, slot_map, cache, k_scale=1.0, v_scale=1.0, err=None, stream
 
     if k.dim() != 3 or cache.dim() != 3:
         raise ValueError("expected k of shape [tokens, kv heads, head_dim] and cache of [pages, kv heads, bytes]")
-    dev, (T, _, D), bf = _cuda_device(k, "k"), k.shape, torch.bfloat16
+    dev, (T, _, D), bf = _cuda_index(k, "k"), k.shape, torch.bfloat16
     cfg = _kv4_config(cache, D, k_scale, v_scale)
     sh = (T, cache.shape[1], D)
-    with _Call(dev, stream, k, v, slot_map, cache, err) as st:
-        _ok(load().rssm_kv4_append(
+
+    def call(st):
+        return load().rssm_kv4_append(
             ctypes.byref(cfg), T, _want("k", k, bf, sh, dev), _want("v", v, bf, sh, dev),
             _want("slot_map", slot_map, torch.int32, (T,), dev), _want("cache", cache, torch.uint8, cache.shape, dev),
-            _opt("err", err, torch.int32, (4,), dev), st), "rssm_kv4_append")
+            _opt("err", err, torch.int32, (4,), dev), st)
+
+    _ok(_run(call, dev, stream, (k, v, slot_map, cache, err)), "rssm_kv4_append")
 
 
 def kv4_export(slot_map, cache, head_dim, k_scale=1.0, v_scale=1.0, k=None, v=None, err=None, stream=None):
@@ -435,19 +446,23 @@ def kv4_export(slot_map, cache, head_dim, k_scale=1.0, v_scale=1.0, k=None, v=No
     (k, v) [tokens, kv heads, head_dim]."""
     import torch
 
-    dev, bf = _cuda_device(slot_map, "slot_map"), torch.bfloat16
+    dev, bf = _cuda_index(slot_map, "slot_map"), torch.bfloat16
     if cache.dim() != 3 or slot_map.dim() != 1:
         raise ValueError("expected slot_map of shape [tokens] and cache of [pages, kv heads, bytes]")
     cfg = _kv4_config(cache, head_dim, k_scale, v_scale)
     T = slot_map.shape[0]
     sh = (T, cache.shape[1], head_dim)
-    with _Call(dev, stream, slot_map, cache, k, v, err) as st:
-        k = torch.empty(sh, dtype=bf, device=dev) if k is None else k
-        v = torch.empty(sh, dtype=bf, device=dev) if v is None else v
-        _ok(load().rssm_kv4_export(
+
+    def call(st):
+        nonlocal k, v
+        k = torch.empty(sh, dtype=bf, device=cache.device) if k is None else k
+        v = torch.empty(sh, dtype=bf, device=cache.device) if v is None else v
+        return load().rssm_kv4_export(
             ctypes.byref(cfg), T, _want("slot_map", slot_map, torch.int32, (T,), dev),
             _want("cache", cache, torch.uint8, cache.shape, dev), _want("k", k, bf, sh, dev),
-            _want("v", v, bf, sh, dev), _opt("err", err, torch.int32, (4,), dev), st), "rssm_kv4_export")
+            _want("v", v, bf, sh, dev), _opt("err", err, torch.int32, (4,), dev), st)
+
+    _ok(_run(call, dev, stream, (slot_map, cache, k, v, err)), "rssm_kv4_export")
     return k, v
 
 
@@ -464,23 +479,24 @@ def kv4_attend(q, cache, block_table, seq_len, cu_q, max_q, k_scale=1.0, v_scale
     if q.dim() != 3 or cache.dim() != 3 or block_table.dim() != 2 or seq_len.dim() != 1:
         raise ValueError("expected q [tokens, heads, head_dim], cache [pages, kv heads, bytes], block_table "
                          "[requests, pages] and seq_len [requests]")
-    dev, (T, Hq, D), bf, i32 = _cuda_device(q, "q"), q.shape, torch.bfloat16, torch.int32
+    dev, (T, Hq, D), bf, i32 = _cuda_index(q, "q"), q.shape, torch.bfloat16, torch.int32
     cfg = _kv4_config(cache, D, k_scale, v_scale)
     Bn, width = block_table.shape
-    att = rssm_attend_config(Bn, Hq, T, width, max_q, width * cfg.page_size if max_seq is None else max_seq,
-                             D ** -0.5 if sm_scale is None else sm_scale)
-    with _Call(dev, stream, q, cache, block_table, seq_len, cu_q, out, workspace, err) as st:
-        out = torch.empty((T, Hq, D), dtype=bf, device=dev) if out is None else out
-        need = int(load().rssm_kv4_attend_workspace_bytes(ctypes.byref(cfg), ctypes.byref(att)))
-        if need and workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        _ok(load().rssm_kv4_attend(
-            ctypes.byref(cfg), ctypes.byref(att), _want("q", q, bf, (T, Hq, D), dev),
-            _want("cache", cache, torch.uint8, cache.shape, dev),
+
+    def call(st):
+        nonlocal out
+        out = torch.empty((T, Hq, D), dtype=bf, device=q.device) if out is None else out
+        lib, kv = load(), ctypes.byref(cfg)
+        att = ctypes.byref(rssm_attend_config(Bn, Hq, T, width, max_q, width * cfg.page_size if max_seq is None else max_seq,
+                                              D ** -0.5 if sm_scale is None else sm_scale))
+        _, ws, nb = _workspace(workspace, lib.rssm_kv4_attend_workspace_bytes(kv, att), dev, q.device)
+        return lib.rssm_kv4_attend(
+            kv, att, _want("q", q, bf, (T, Hq, D), dev), _want("cache", cache, torch.uint8, cache.shape, dev),
             _want("block_table", block_table, i32, (Bn, width), dev), _want("seq_len", seq_len, i32, (Bn,), dev),
-            _want("cu_q", cu_q, i32, (Bn + 1,), dev), _want("out", out, bf, (T, Hq, D), dev),
-            _opt("workspace", workspace, torch.uint8, (None,), dev), 0 if workspace is None else workspace.shape[0],
-            _opt("err", err, i32, (4,), dev), st), "rssm_kv4_attend")
+            _want("cu_q", cu_q, i32, (Bn + 1,), dev), _want("out", out, bf, (T, Hq, D), dev), ws, nb,
+            _opt("err", err, i32, (4,), dev), st)
+
+    _ok(_run(call, dev, stream, (q, cache, block_table, seq_len, cu_q, out, workspace, err)), "rssm_kv4_attend")
     return out
 
 
