@@ -114,6 +114,7 @@ __global__ void __launch_bounds__(kChunkThreads, 4) gdn_chunk_kernel(const GdnPr
     int *sfound = reinterpret_cast<int *>(bar + 2);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int slot = blockIdx.x, h = blockIdx.y, H = a.H;
+    pdl_trigger();  // the scan's CTAs may start: they read this kernel's results behind their own wait
 
     // The request of this slot: the last b with cu[b] / 64 + b <= slot, 32 candidates a round.
     if (warp == 0) {
@@ -145,6 +146,15 @@ __global__ void __launch_bounds__(kChunkThreads, 4) gdn_chunk_kernel(const GdnPr
     bool failed = false;
     if (work) {
         const int Lc = min(kC, r1 - t0);
+        float al[2] = {1.f, 1.f}, be[2] = {0.f, 0.f};  // gates of tokens 2 lane, 2 lane + 1
+        if (warp == 0) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                if (2 * lane + e < Lc) {
+                    al[e] = a.alpha[(int64_t)(t0 + 2 * lane + e) * H + h];
+                    be[e] = a.beta[(int64_t)(t0 + 2 * lane + e) * H + h];
+                }
+        }
         // K and Q rows, 16 lanes a row, 16 rows a round; rows behind the prompt are zero.
         {
             const int r = tid >> 4, ch = tid & 15;
@@ -160,17 +170,12 @@ __global__ void __launch_bounds__(kChunkThreads, 4) gdn_chunk_kernel(const GdnPr
         }
         cp_async_commit();
         if (warp == 0) {
-            // Lam: lane l has tokens 2l, 2l + 1.  A gate of 0 counts as 2^-200, which is 0 in every
+            // Lam.  A gate of 0 counts as 2^-200, which is 0 in every
             // fp32 product that it enters.
             double v[2];
-            float be[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int t = 2 * lane + e;
-                const bool live = t < Lc;
-                const float al = live ? a.alpha[(int64_t)(t0 + t) * H + h] : 1.f;
-                be[e] = live ? a.beta[(int64_t)(t0 + t) * H + h] : 0.f;
-                const float lg = log2f(al);
+                const float lg = log2f(al[e]);
                 v[e] = (double)(lg < -200.f ? -200.f : lg);
             }
             double x = v[0] + v[1];
@@ -227,22 +232,26 @@ __global__ void __launch_bounds__(kChunkThreads, 4) gdn_chunk_kernel(const GdnPr
                 float gv[16];
                 if (blk <= last_blk) {  // warp-uniform
                     tmem_ld16(base + j0, gv);
-                    const float f = bi * ex2((li - lamh[j0 + 15]) + (ll - laml[j0 + 15]));
-                    const bool diag = (i >> 4) == blk;
+                    if ((i >> 4) == blk) {
 #pragma unroll
-                    for (int j = 0; j < 16; j += 4) {
-                        const float4 g4 = *reinterpret_cast<const float4 *>(sg + j0 + j);
-                        float w[4] = {f * g4.x, f * g4.y, f * g4.z, f * g4.w};
-                        if (diag) {
+                        for (int j = 0; j < 16; j += 4) {
                             const float4 h4 = *reinterpret_cast<const float4 *>(lamh + j0 + j);
                             const float4 l4 = *reinterpret_cast<const float4 *>(laml + j0 + j);
-                            w[0] = bi * ex2((li - h4.x) + (ll - l4.x));
-                            w[1] = bi * ex2((li - h4.y) + (ll - l4.y));
-                            w[2] = bi * ex2((li - h4.z) + (ll - l4.z));
-                            w[3] = bi * ex2((li - h4.w) + (ll - l4.w));
-                        }
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) gv[j + e] = j0 + j + e < lim ? w[e] * gv[j + e] : 0.f;
+                            for (int e = 0; e < 4; ++e) {
+                                const float w = bi * ex2((li - (&h4.x)[e]) + (ll - (&l4.x)[e]));
+                                gv[j + e] = j0 + j + e < lim ? w * gv[j + e] : 0.f;
+                            }
+                        }
+                    } else {
+                        const bool left = (i >> 4) > blk;
+                        const float f = left ? bi * ex2((li - lamh[j0 + 15]) + (ll - laml[j0 + 15])) : 0.f;
+#pragma unroll
+                        for (int j = 0; j < 16; j += 4) {
+                            const float4 g4 = *reinterpret_cast<const float4 *>(sg + j0 + j);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) gv[j + e] = left ? f * (&g4.x)[e] * gv[j + e] : 0.f;
+                        }
                     }
                 } else {
 #pragma unroll
@@ -677,6 +686,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const GdnPreA
             load(c);
             if (c >= 2 && !wait_for(kBarO, c & 1)) break;   // and its decays read
             if (warp == kFirstIn && lane == 0) {
+                if (c == 0) pdl_wait();  // the chunk kernel's operands are there
                 uint64_t *br = bar + kBarOp + (c & 1);
                 mbar_arrive_expect_tx(br, kSlot);
                 bulk_g2s(sm + L::kOp + (c & 1) * L::kOpStep, a.ws + ((int64_t)(r0 / kC + b + c) * H + h) * kSlot, kSlot, br);
@@ -766,8 +776,17 @@ cudaError_t gdn_chunk_launch(const GdnPreArgs &a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     gdn_chunk_kernel<<<dim3((unsigned)slots(a.B, a.tokens), a.H), kChunkThreads, s1, st>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    gdn_scan_kernel<<<dim3(a.H * ((a.P + 127) / 128), a.B), kScanThreads, s2, st>>>(a);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(a.H * ((a.P + 127) / 128), a.B);
+    cfg.blockDim = dim3(kScanThreads);
+    cfg.dynamicSmemBytes = s2;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, gdn_scan_kernel, a);
 }
 
 }  // namespace rssm

@@ -134,6 +134,7 @@ __global__ void __launch_bounds__(32 * kWarps4, MT == 1 ? 3 : 2) attend_kernel(c
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
     const int split = blockIdx.x, tile = blockIdx.y % a.tiles, h = blockIdx.y / a.tiles, b = blockIdx.z;
     const int ps = a.kv.ps, G = a.G;
+    if (a.splits > 1) pdl_trigger();  // the joining kernel's CTAs may start, up to their wait
     int r0, n, len;
     if (!attend_request(a, b, r0, n, len)) {
         if (tid == 0) report_opt(a.err, DEV_BAD_LENGTHS, b, 0, len);
@@ -557,6 +558,7 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttendArgs a) {
     const int last = min(row0 + RT, rows) - 1;
     const int ns = (max(0, len - n + last / a.G + 1) + a.L - 1) / a.L;
     if (ns <= 1) return;
+    pdl_wait();
     const int64_t unit = (((int64_t)b * a.kv.Hk + h) * a.tiles + tile) * a.splits;
     const float2 *ml = reinterpret_cast<const float2 *>(a.part + (int64_t)a.B * a.kv.Hk * a.tiles * a.splits * RT * D);
     for (int r = threadIdx.x / TPR; r < min(RT, rows - row0); r += 256 / TPR) {
@@ -625,8 +627,16 @@ cudaError_t attend_launch(const AttendArgs &a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     attend_kernel<D, MT><<<dim3(a.splits, a.tiles * a.kv.Hk, a.B), 32 * kWarps4, Smem<D, MT>::kBytes, st>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess || a.splits == 1) return e;
-    attend_join_kernel<D, MT><<<dim3(a.tiles * a.kv.Hk, a.B), 256, 0, st>>>(a);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(a.tiles * a.kv.Hk, a.B);
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attend_join_kernel<D, MT>, a);
 }
 
 }  // namespace
