@@ -56,36 +56,9 @@ __device__ __forceinline__ void split8(const float *v, uint4 &hi, uint4 &lo) {
         pl[e] = bf16x2(v[2 * e] - __uint_as_float(h << 16), v[2 * e + 1] - __uint_as_float(h & 0xffff0000u));
     }
 }
-__device__ __forceinline__ float ex2(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
 __device__ __forceinline__ void bulk_s2g(void *dst, const void *src, uint32_t bytes) {
     asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
                  : "memory");
-}
-
-// A wait on a barrier's phase gives up after this many cycles (2 s at 2 GHz).
-constexpr long long kWaitCycles = 4000000000ll;
-
-// try_wait that may sleep for up to 1 ms: a dozen waiting warps that poll take the shared-memory pipe from the
-// warps that work.
-__device__ __forceinline__ bool bar_try(uint64_t *bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u)
-        : "memory");
-    return ok != 0;
-}
-__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity) {
-    if (bar_try(bar, parity)) return true;
-    const long long t0 = clock64();
-    while (!bar_try(bar, parity))
-        if (clock64() - t0 > kWaitCycles) return false;
-    return true;
 }
 
 // ---------------------------------------------------------------- chunk operands
@@ -470,6 +443,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const GdnPreA
     int r0, r1;
     if (!packed_rows(a.cu, b, a.tokens, r0, r1)) {
         if (tid == 0) report_opt(a.err, DEV_BAD_LENGTHS, b, h, r1);
+        pdl_wait();  // no CTA ends before the chunk kernel has
         return;
     }
     if (warp == 0) tmem_alloc(tslot, 512);
@@ -681,12 +655,12 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const GdnPreA
                 src += step;
             }
         };
+        if (warp == kFirstIn) pdl_wait();  // the chunk kernel's operands are there
         for (int c = 0; c < nchunks; ++c) {
             if (c >= 2 && !wait_for(kBarZq, c & 1)) break;  // chunk c - 2's products are done
             load(c);
             if (c >= 2 && !wait_for(kBarO, c & 1)) break;   // and its decays read
             if (warp == kFirstIn && lane == 0) {
-                if (c == 0) pdl_wait();  // the chunk kernel's operands are there
                 uint64_t *br = bar + kBarOp + (c & 1);
                 mbar_arrive_expect_tx(br, kSlot);
                 bulk_g2s(sm + L::kOp + (c & 1) * L::kOpStep, a.ws + ((int64_t)(r0 / kC + b + c) * H + h) * kSlot, kSlot, br);
@@ -710,7 +684,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const GdnPreA
                 for (int hl = 0; hl < 2; ++hl)
 #pragma unroll
                     for (int ks = 0; ks < kDk / 16; ++ks)
-                        umma_bf16_ts(tmem + kTmY + q * kC, tmem + kTmA + 64 * hl + 8 * ks,
+                        umma_ts(tmem + kTmY + q * kC, tmem + kTmA + 64 * hl + 8 * ks,
                                      sw128_desc_of(kq + (q * kC * 128 + (ks >> 2) * kTile + (ks & 3) * 32) / 16),
                                      idesc_bf16_f32(128, kC), hl > 0 || ks > 0);
             };
@@ -719,7 +693,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const GdnPreA
                 for (int pr = 0; pr < 3; ++pr)
 #pragma unroll
                     for (int ks = 0; ks < kC / 16; ++ks)
-                        umma_bf16_ts(d, tmem + kTmR + (pr == 2 ? 32 : 0) + 8 * ks,
+                        umma_ts(d, tmem + kTmR + (pr == 2 ? 32 : 0) + 8 * ks,
                                      sw128_desc_of(op + (q * kC * 128 + (pr == 1 ? kTile : 0) + ks * 32) / 16),
                                      idesc_bf16_f32(128, kC), pr > 0 || ks > 0);
             };
@@ -741,7 +715,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const GdnPreA
                 for (int hl = 0; hl < 2; ++hl)  // S += (w U)^T K
 #pragma unroll
                     for (int ks = 0; ks < kC / 16; ++ks)
-                        umma_bf16_ts(tmem + kTmS, tmem + kTmY + 16 * ks + 8 * hl, sw128_desc_of(kt + ks * 2048 / 16),
+                        umma_ts(tmem + kTmS, tmem + kTmY + 16 * ks + 8 * hl, sw128_desc_of(kt + ks * 2048 / 16),
                                      idesc_bf16_f32_mn(128, kDk, false, true), true);
                 umma_commit(bar + kBarS);
                 z_products(tmem + kTmZq, 1);

@@ -25,34 +25,19 @@
 // CTA's range, by asynchronous copies into a ring of kStages stages of its own; the warps of a
 // CTA meet only at the end, to join their sums.  Long contexts are split over CTAs and
 // joined by a second kernel.
-#include <cuda_bf16.h>
-
 #include <math.h>
 
 #include "rssm_internal.h"
-#include "rssm_kv4.cuh"
+#include "rssm_kv4_attend.cuh"
+#include "rssm_umma.cuh"
 
 namespace rssm {
 
 namespace {
 
-struct AttendArgs {
-    Kv4Args kv;
-    int B, Hq, G, tokens, max_pages, max_q, max_seq;
-    int tiles, splits, L;  // row tiles a request, splits, cached tokens a split
-    float scale;           // sm_scale * k_scale * log2(e)
-    const __nv_bfloat16 *q;
-    const uint8_t *cache;
-    const int32_t *table, *seq_len, *cu;
-    __nv_bfloat16 *out;
-    float *part;  // [B][Hk][tiles][splits][rows][D], then (m, l) [...][rows][2]
-    int32_t *err;
-};
-
 constexpr int kWarps4 = 4;
 constexpr int kStages = 3;
 constexpr int kStep = 32;        // tokens a warp takes at a time
-constexpr float kLag = 6.f;      // log2 by which the running maximum may trail
 
 template <int D> struct Ring {
     static constexpr int kGran = 16 * D * 9 / 8;           // 16 tokens: K codes, K scales, V codes, V scales
@@ -70,58 +55,12 @@ template <int D, int MT> struct Smem {
     static constexpr int kBytes = kRow + MT * 16 * 8;          // score factor and visible tokens of every row
 };
 
-// The rows and length of request b; false (and reported) where they do not fit the call.
-__device__ __forceinline__ bool attend_request(const AttendArgs &a, int b, int &r0, int &n, int &len) {
-    int r1;
-    const bool ok = packed_rows(a.cu, b, a.tokens, r0, r1);
-    n = r1 - r0;
-    len = a.seq_len[b];
-    return ok && n <= a.max_q && len >= 0 && len <= a.max_seq && len <= (int64_t)a.max_pages * a.kv.ps;
-}
-
-__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-__device__ __forceinline__ float ex2(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-// The four bytes of w, two e2m1 codes each, as fp16 pairs.
-__device__ __forceinline__ void widen(uint32_t w, uint32_t (&h)[4]) {
-    asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %4;\n cvt.rn.f16x2.e2m1x2 %0, a;\n"
-        " cvt.rn.f16x2.e2m1x2 %1, b;\n cvt.rn.f16x2.e2m1x2 %2, c;\n cvt.rn.f16x2.e2m1x2 %3, d;\n}\n"
-        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-        : "r"(w));
-}
-// Two e4m3 bytes (low 16 bits of w) as an fp16 pair.
-__device__ __forceinline__ uint32_t scales2(uint32_t w) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)w));
-    return r;
-}
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-
-// A row's power-of-two scale: the largest magnitude goes to [2^9, 2^10).
-__device__ __forceinline__ int row_exponent(float top) {
-    const int e = (int)(__float_as_uint(top) >> 23);  // top >= 0
-    return e == 0 || e == 255 ? 0 : e - 126 - 10;
-}
-
-// 2^e for e in -126 .. 127.
-__device__ __forceinline__ float pow2f(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
 template <int D, int MT>
 __global__ void __launch_bounds__(32 * kWarps4, MT == 1 ? 3 : 2) attend_kernel(const AttendArgs a) {
@@ -551,6 +490,7 @@ template <int D, int MT>
 __global__ void __launch_bounds__(256) attend_join_kernel(const AttendArgs a) {
     constexpr int RT = 16 * MT, TPR = D / 4;  // threads a row, 4 channels each
     const int tile = blockIdx.x % a.tiles, h = blockIdx.x / a.tiles, b = blockIdx.y;
+    pdl_wait();  // first of all: no CTA ends before the kernel whose results it joins
     int r0, n, len;
     if (!attend_request(a, b, r0, n, len)) return;  // reported by the first kernel
     const int rows = n * a.G, row0 = tile * RT;
@@ -558,7 +498,6 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttendArgs a) {
     const int last = min(row0 + RT, rows) - 1;
     const int ns = (max(0, len - n + last / a.G + 1) + a.L - 1) / a.L;
     if (ns <= 1) return;
-    pdl_wait();
     const int64_t unit = (((int64_t)b * a.kv.Hk + h) * a.tiles + tile) * a.splits;
     const float2 *ml = reinterpret_cast<const float2 *>(a.part + (int64_t)a.B * a.kv.Hk * a.tiles * a.splits * RT * D);
     for (int r = threadIdx.x / TPR; r < min(RT, rows - row0); r += 256 / TPR) {
@@ -585,6 +524,7 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttendArgs a) {
 float score_scale(float sm_scale, float k_scale) { return sm_scale * k_scale * 1.4426950408889634f; }
 
 constexpr int64_t kMaxL = 2048, kWaves = 2;
+constexpr int64_t kTileRows = 32;  // more rows than this go to the kernel for tiles of 128
 
 // Sizes of the launch.  Row tiles of 32 where a request can have more than 16 rows.
 struct Plan {
@@ -601,17 +541,17 @@ bool attend_plan(const rssm_kv4_config *c, const rssm_attend_config *t, Kv4Args 
     const int64_t max_q = t->max_q < t->tokens ? t->max_q : t->tokens;
     const int64_t rows = max_q * (t->n_q_heads / kv->Hk);
     if (rows > 0x3fffffff) return false;
-    p->mt = rows > 16 ? 2 : 1;
+    p->mt = rows > kTileRows ? 8 : rows > 16 ? 2 : 1;
     const int64_t tiles = (rows + 16 * p->mt - 1) / (16 * p->mt);
     if (tiles * kv->Hk > 65535) return false;
     int64_t seq = (int64_t)t->max_pages * kv->ps;
     if (t->max_seq < seq) seq = t->max_seq;
     // Tokens of one CTA: a share of the work that fills the machine (148 SMs, 3 CTAs each) several times over,
     // between 256 (a shorter one is all start and join) and kMaxL (a longer one makes a long tail).
-    const int64_t units = (int64_t)t->batch * kv->Hk * tiles, want = 148 * 3 * kWaves;
+    const int64_t units = (int64_t)t->batch * kv->Hk * tiles, want = 148 * (p->mt == 8 ? 1 : 3) * kWaves;
     int64_t L = (seq * units + want - 1) / want;
     L = L < 256 ? 256 : L > kMaxL ? kMaxL : L;
-    if (tiles > 4) L = seq;  // a prompt chunk: its tiles fill the machine
+    if (p->mt == 8 && units >= want) L = seq;  // a prompt chunk whose tiles fill the machine
     L = (L + 127) / 128 * 128;
     const int64_t splits = (seq + L - 1) / L;
     p->tiles = (int)tiles;
@@ -622,11 +562,7 @@ bool attend_plan(const rssm_kv4_config *c, const rssm_attend_config *t, Kv4Args 
 }
 
 template <int D, int MT>
-cudaError_t attend_launch(const AttendArgs &a, cudaStream_t st) {
-    cudaError_t e = cudaFuncSetAttribute(attend_kernel<D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D, MT>::kBytes);
-    if (e != cudaSuccess) return e;
-    attend_kernel<D, MT><<<dim3(a.splits, a.tiles * a.kv.Hk, a.B), 32 * kWarps4, Smem<D, MT>::kBytes, st>>>(a);
-    if ((e = cudaGetLastError()) != cudaSuccess || a.splits == 1) return e;
+cudaError_t join_launch(const AttendArgs &a, cudaStream_t st) {
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -637,6 +573,21 @@ cudaError_t attend_launch(const AttendArgs &a, cudaStream_t st) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, attend_join_kernel<D, MT>, a);
+}
+
+template <int D, int MT>
+cudaError_t attend_launch(const AttendArgs &a, cudaStream_t st) {
+    cudaError_t e;
+    if constexpr (MT == 8) {
+        if ((e = attend_tiles_launch(a, st)) != cudaSuccess || a.splits == 1) return e;
+        return join_launch<D, MT>(a, st);
+    } else {
+    e = cudaFuncSetAttribute(attend_kernel<D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D, MT>::kBytes);
+    if (e != cudaSuccess) return e;
+    attend_kernel<D, MT><<<dim3(a.splits, a.tiles * a.kv.Hk, a.B), 32 * kWarps4, Smem<D, MT>::kBytes, st>>>(a);
+    if ((e = cudaGetLastError()) != cudaSuccess || a.splits == 1) return e;
+    return join_launch<D, MT>(a, st);
+    }
 }
 
 }  // namespace
@@ -670,8 +621,9 @@ RSSM_API rssm_status rssm_kv4_attend(const rssm_kv4_config *cfg, const rssm_atte
     a.table = block_table; a.seq_len = seq_len; a.cu = cu_q; a.out = (__nv_bfloat16 *)out; a.part = (float *)workspace;
     a.err = dev_error;
     const cudaStream_t st = (cudaStream_t)stream;
-    const cudaError_t e = a.kv.D == 64 ? (p.mt == 1 ? attend_launch<64, 1>(a, st) : attend_launch<64, 2>(a, st))
-                                       : (p.mt == 1 ? attend_launch<128, 1>(a, st) : attend_launch<128, 2>(a, st));
+    const cudaError_t e =
+        a.kv.D == 64 ? (p.mt == 1 ? attend_launch<64, 1>(a, st) : p.mt == 2 ? attend_launch<64, 2>(a, st) : attend_launch<64, 8>(a, st))
+                     : (p.mt == 1 ? attend_launch<128, 1>(a, st) : p.mt == 2 ? attend_launch<128, 2>(a, st) : attend_launch<128, 8>(a, st));
     return e == cudaSuccess ? RSSM_OK : RSSM_ECUDA;
 }
 
