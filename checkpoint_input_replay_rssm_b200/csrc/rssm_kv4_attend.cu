@@ -524,7 +524,7 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttendArgs a) {
 float score_scale(float sm_scale, float k_scale) { return sm_scale * k_scale * 1.4426950408889634f; }
 
 constexpr int64_t kMaxL = 2048, kWaves = 2;
-constexpr int64_t kTileRows = 32;  // more rows than this go to the kernel for tiles of 128
+constexpr int64_t kTileRows = 128, kTileUnits = 32;
 
 // Sizes of the launch.  Row tiles of 32 where a request can have more than 16 rows.
 struct Plan {
@@ -541,17 +541,19 @@ bool attend_plan(const rssm_kv4_config *c, const rssm_attend_config *t, Kv4Args 
     const int64_t max_q = t->max_q < t->tokens ? t->max_q : t->tokens;
     const int64_t rows = max_q * (t->n_q_heads / kv->Hk);
     if (rows > 0x3fffffff) return false;
-    p->mt = rows > kTileRows ? 8 : rows > 16 ? 2 : 1;
+    // Tiles of 128 rows where a request has as many and there are enough of them; they are not split.
+    const int64_t big = (rows + 127) / 128;
+    p->mt = rows >= kTileRows && (int64_t)t->batch * kv->Hk * big >= kTileUnits ? 8 : rows > 16 ? 2 : 1;
     const int64_t tiles = (rows + 16 * p->mt - 1) / (16 * p->mt);
-    if (tiles * kv->Hk > 65535) return false;
+    if (p->mt != 8 && tiles * kv->Hk > 65535) return false;
     int64_t seq = (int64_t)t->max_pages * kv->ps;
     if (t->max_seq < seq) seq = t->max_seq;
-    // Tokens of one CTA: a share of the work that fills the machine (148 SMs, 3 CTAs each) several times over,
+    // Tokens of one CTA: a share of the work that fills the machine (148 SMs, 3 CTAs each) kWaves times over,
     // between 256 (a shorter one is all start and join) and kMaxL (a longer one makes a long tail).
-    const int64_t units = (int64_t)t->batch * kv->Hk * tiles, want = 148 * (p->mt == 8 ? 1 : 3) * kWaves;
+    const int64_t units = (int64_t)t->batch * kv->Hk * tiles, want = 148 * 3 * kWaves;
     int64_t L = (seq * units + want - 1) / want;
     L = L < 256 ? 256 : L > kMaxL ? kMaxL : L;
-    if (p->mt == 8 && units >= want) L = seq;  // a prompt chunk whose tiles fill the machine
+    if (p->mt == 8) L = seq;
     L = (L + 127) / 128 * 128;
     const int64_t splits = (seq + L - 1) / L;
     p->tiles = (int)tiles;
@@ -562,7 +564,11 @@ bool attend_plan(const rssm_kv4_config *c, const rssm_attend_config *t, Kv4Args 
 }
 
 template <int D, int MT>
-cudaError_t join_launch(const AttendArgs &a, cudaStream_t st) {
+cudaError_t attend_launch(const AttendArgs &a, cudaStream_t st) {
+    cudaError_t e = cudaFuncSetAttribute(attend_kernel<D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D, MT>::kBytes);
+    if (e != cudaSuccess) return e;
+    attend_kernel<D, MT><<<dim3(a.splits, a.tiles * a.kv.Hk, a.B), 32 * kWarps4, Smem<D, MT>::kBytes, st>>>(a);
+    if ((e = cudaGetLastError()) != cudaSuccess || a.splits == 1) return e;
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -573,21 +579,6 @@ cudaError_t join_launch(const AttendArgs &a, cudaStream_t st) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, attend_join_kernel<D, MT>, a);
-}
-
-template <int D, int MT>
-cudaError_t attend_launch(const AttendArgs &a, cudaStream_t st) {
-    cudaError_t e;
-    if constexpr (MT == 8) {
-        if ((e = attend_tiles_launch(a, st)) != cudaSuccess || a.splits == 1) return e;
-        return join_launch<D, MT>(a, st);
-    } else {
-    e = cudaFuncSetAttribute(attend_kernel<D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D, MT>::kBytes);
-    if (e != cudaSuccess) return e;
-    attend_kernel<D, MT><<<dim3(a.splits, a.tiles * a.kv.Hk, a.B), 32 * kWarps4, Smem<D, MT>::kBytes, st>>>(a);
-    if ((e = cudaGetLastError()) != cudaSuccess || a.splits == 1) return e;
-    return join_launch<D, MT>(a, st);
-    }
 }
 
 }  // namespace
@@ -621,9 +612,10 @@ RSSM_API rssm_status rssm_kv4_attend(const rssm_kv4_config *cfg, const rssm_atte
     a.table = block_table; a.seq_len = seq_len; a.cu = cu_q; a.out = (__nv_bfloat16 *)out; a.part = (float *)workspace;
     a.err = dev_error;
     const cudaStream_t st = (cudaStream_t)stream;
-    const cudaError_t e =
-        a.kv.D == 64 ? (p.mt == 1 ? attend_launch<64, 1>(a, st) : p.mt == 2 ? attend_launch<64, 2>(a, st) : attend_launch<64, 8>(a, st))
-                     : (p.mt == 1 ? attend_launch<128, 1>(a, st) : p.mt == 2 ? attend_launch<128, 2>(a, st) : attend_launch<128, 8>(a, st));
+    const bool wide = a.kv.D == 128;
+    const cudaError_t e = p.mt == 8   ? attend_tiles_launch(a, st)
+                          : p.mt == 2 ? (wide ? attend_launch<128, 2>(a, st) : attend_launch<64, 2>(a, st))
+                                      : (wide ? attend_launch<128, 1>(a, st) : attend_launch<64, 1>(a, st));
     return e == cudaSuccess ? RSSM_OK : RSSM_ECUDA;
 }
 

@@ -10,8 +10,8 @@
 // end.  The exponentials (16 a cycle and SM) and the products (2 x 512 cycles a tile at D = 128) are both near 1000
 // cycles a tile, and the rest of the work is laid beside them on warps of their own.
 //
-// Roles: 8 softmax warps (4 a stream), 4 widening warps (one token a thread, the next tile's bytes in registers ahead),
-// 1 issuing warp.  They meet on barriers in shared memory; every wait is bounded.
+// Roles: 8 softmax warps (4 a stream, the first of which issues the stream's products) and 8 widening warps (16 tokens
+// each, the next tile's bytes in registers ahead).  They meet on barriers in shared memory; every wait is bounded.
 #include <math.h>
 
 #include "rssm_internal.h"
@@ -22,9 +22,8 @@ namespace rssm {
 
 namespace {
 
-constexpr int kSoftWarps = 8, kWideWarps = 4;
-constexpr int kWide0 = kSoftWarps, kTilesIssuer = kSoftWarps + kWideWarps;
-constexpr int kTilesThreads = 32 * (kTilesIssuer + 1);
+constexpr int kSoftWarps = 8, kWideWarps = 8, kWide0 = kSoftWarps;
+constexpr int kTilesThreads = 32 * (kSoftWarps + kWideWarps);
 enum TilesBar {
     kBarK = 0,    // K tile written, per stream (every widening warp)
     kBarVt = 2,   // V tile written
@@ -34,8 +33,8 @@ enum TilesBar {
     kBarPv = 9,   // O updated, per stream
     kBarMl = 11,  // maxima and sums written (every softmax warp)
     kBarJoin = 12,  // the second stream's O written (its four warps)
-    kBarDrain = 13,
-    kTilesBars = 14
+    kBarDrain = 13,  // everything issued, per stream, after a failure
+    kTilesBars = 15
 };
 
 template <int D> struct TilesSmem {
@@ -63,9 +62,8 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
     int *snan = reinterpret_cast<int *>(sm + L::kNan);
     uint32_t *sgone = reinterpret_cast<uint32_t *>(sm + L::kGone);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int split = blockIdx.x, tile = blockIdx.y % a.tiles, h = blockIdx.y / a.tiles, b = blockIdx.z;
+    const int tile = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
     const int ps = a.kv.ps, G = a.G;
-    if (a.splits > 1) pdl_trigger();  // the joining kernel's CTAs may start, up to their wait
     int r0, n, len;
     if (!attend_request(a, b, r0, n, len)) {
         if (tid == 0) report_opt(a.err, DEV_BAD_LENGTHS, b, 0, len);
@@ -74,11 +72,8 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
     const int rows = n * G, row0 = tile * 128;
     if (row0 >= rows) return;
     const int last = min(row0 + 128, rows) - 1;
-    const int tlen = max(0, len - n + last / G + 1);  // tokens that the tile's last row sees
-    const int ns = max(1, (tlen + a.L - 1) / a.L);
-    if (split >= ns) return;
-    const int t_begin = split * a.L, t_end = min(tlen, t_begin + a.L);
-    const int ntiles = (t_end - t_begin + 127) / 128;
+    const int t_end = max(0, len - n + last / G + 1);  // tokens that the tile's last row sees
+    const int ntiles = (t_end + 127) / 128;
 
     if (warp == 0) tmem_alloc(tslot, 512);
     if (tid == 0) {
@@ -121,13 +116,16 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
         {
             // This row of Q, scaled by a power of two (see rssm_kv4_attend.cu); the first stream's threads write it.
             const uint4 *src = reinterpret_cast<const uint4 *>(a.q + q_at);
+            if (!live) src = reinterpret_cast<const uint4 *>(a.q);  // any row: its scores are masked
+            uint4 v[D / 8];
+#pragma unroll
+            for (int k = 0; k < D / 8; ++k) v[k] = src[k];
             float top = 0.f;
-#pragma unroll 4
+#pragma unroll
             for (int k = 0; k < D / 8; ++k) {
-                const uint4 v = live ? src[k] : make_uint4(0, 0, 0, 0);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const uint32_t x = (&v.x)[e];
+                    const uint32_t x = (&v[k].x)[e];
                     top = fmaxf(top, fmaxf(fabsf(bf16_bits_to_float(x & 0xffff)), fabsf(bf16_bits_to_float(x >> 16))));
                 }
             }
@@ -136,13 +134,12 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
             const float s1 = a.scale == 0.f ? 0.f : pow2f(-(ex - ex / 2));
             f = fmaxf(fabsf(a.scale) * pow2f(ex / 2) * pow2f(ex - ex / 2), 1.2e-38f);
             if (st == 0) {
-#pragma unroll 4
+#pragma unroll
                 for (int k = 0; k < D / 8; ++k) {
-                    const uint4 v = live ? src[k] : make_uint4(0, 0, 0, 0);
                     uint4 w;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const uint32_t x = (&v.x)[e];
+                        const uint32_t x = (&v[k].x)[e];
                         (&w.x)[e] = f16x2(bf16_bits_to_float(x & 0xffff) * s0 * s1, bf16_bits_to_float(x >> 16) * s0 * s1);
                     }
                     *reinterpret_cast<uint4 *>(sm + L::kQ + sw128_chunk(row, k, 128)) = w;
@@ -152,28 +149,65 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
             }
         }
         const uint32_t s_tm = base + 128 * st, o_tm = base + kTmO + D * st;
+        // The products of this stream, issued by one thread of its first warp.
+        const bool issues = (warp & 3) == 0, lead = issues && elect_one();
+        const uint32_t smem0 = smem_u32(sm), q = sw128_desc_lo(smem0 + L::kQ);
+        const uint32_t kd = sw128_desc_lo(smem0 + L::kKt + st * L::kTileB), vd = sw128_desc_lo(smem0 + L::kVt + st * L::kTileB, 128 * 128);
+        auto scores = [&] {
+            if (lead) {
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    const uint32_t at = ((ks >> 2) * 128 * 128 + (ks & 3) * 32) / 16;
+                    umma_bf16(tmem + 128 * st, sw128_desc_of(q + at), sw128_desc_of(kd + at), idesc_f16_f32(128, 128, false), ks > 0);
+                }
+                umma_commit(bar + kBarSc + st);
+            }
+            __syncwarp();
+        };
+        auto output = [&](bool more) {
+            if (lead) {
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks)
+                    umma_ts(tmem + kTmO + D * st, tmem + 128 * st + 8 * ks, sw128_desc_of(vd + ks * 2048 / 16),
+                            idesc_f16_f32(128, D, true), more || ks > 0);
+                umma_commit(bar + kBarPv + st);
+            }
+            __syncwarp();
+        };
         float m = -INFINITY, l = 0.f;
         bool ok = true;
-        for (int j = st; j < ntiles; j += 2) {
-            const int k = j >> 1, t0 = t_begin + 128 * j;
+        if (issues && st < ntiles) {
+            ok = wait_for(kBarQ, 0) && wait_for(kBarK + st, 0);
+            if (ok) scores();
+        }
+        for (int j = st; ok && j < ntiles; j += 2) {
+            const int k = j >> 1, t0 = 128 * j;
             if (!(ok = wait_for(kBarSc + st, k & 1))) break;
             const int lim = min(seen, t_end) - t0;  // columns below lim are seen
             const uint32_t *gone = sgone + 4 * (j & 3);
             const bool edge = __any_sync(0xffffffffu, lim < 128) || (gone[0] | gone[1] | gone[2] | gone[3]);
-            float top = -INFINITY;
-#pragma unroll 1
-            for (int c = 0; c < 128; c += 32) {
-                float x[32];
-                tmem_ld32(s_tm + c, x);
+            // Two passes over S (the maximum, then P, which takes S's place), 16 columns under way while 16 are worked on.
+            float x[2][16], top = -INFINITY;
+            auto masked = [&](int c, float(&y)[16]) {
                 if (edge) {
-                    const uint32_t gw = gone[c >> 5];
+                    const uint32_t gw = gone[c >> 1] >> (16 * (c & 1));
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (c + e >= lim || (gw >> e & 1)) x[e] = -INFINITY;
+                    for (int e = 0; e < 16; ++e)
+                        if (16 * c + e >= lim || (gw >> e & 1)) y[e] = -INFINITY;
                 }
+            };
+            tmem_ld16_start(s_tm, x[0]);
+#pragma unroll 1
+            for (int c2 = 0; c2 < 8; c2 += 2)
 #pragma unroll
-                for (int e = 0; e < 32; ++e) top = fmaxf(top, x[e]);
-            }
+                for (int u = 0; u < 2; ++u) {
+                    const int c = c2 + u;
+                    tmem_ld_wait(x[u]);
+                    tmem_ld16_start(s_tm + 16 * ((c + 1) & 7), x[u ^ 1]);  // the last one is the second pass's first
+                    masked(c, x[u]);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) top = fmaxf(top, x[u][e]);
+                }
             top *= f;
             if (__any_sync(0xffffffffu, top > m + kLag)) {
                 const float mn = fmaxf(m, top), fac = mn == -INFINITY ? 1.f : ex2(m - mn);
@@ -182,38 +216,45 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
                 if (k > 0) {
                     if (!(ok = wait_for(kBarPv + st, (k - 1) & 1))) break;
 #pragma unroll 1
-                    for (int c = 0; c < D; c += 32) {
-                        float x[32];
-                        tmem_ld32(o_tm + c, x);
+                    for (int c = 0; c < D; c += 16) {
+                        float o[16];
+                        tmem_ld16(o_tm + c, o);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) x[e] *= fac;
-                        tmem_st32(o_tm + c, x);
+                        for (int e = 0; e < 16; ++e) o[e] *= fac;
+                        tmem_st16(o_tm + c, o);
                     }
                 }
             }
             const float off = m == -INFINITY ? 0.f : m;  // a row that has seen nothing yet keeps p = 2^-inf = 0
 #pragma unroll 1
-            for (int c = 0; c < 128; c += 32) {
-                float x[32];
-                uint32_t w[16];
-                tmem_ld32(s_tm + c, x);
-                if (edge) {
-                    const uint32_t gw = gone[c >> 5];
+            for (int c2 = 0; c2 < 8; c2 += 2)
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (c + e >= lim || (gw >> e & 1)) x[e] = -INFINITY;
+                for (int u = 0; u < 2; ++u) {
+                    const int c = c2 + u;
+                    float(&y)[16] = x[u];
+                    tmem_ld_wait(y);
+                    if (c < 7) tmem_ld16_start(s_tm + 16 * (c + 1), x[u ^ 1]);
+                    masked(c, y);
+                    uint32_t w[8];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        y[e] = ex2(fmaf(y[e], f, -off));
+                        l += y[e];
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) w[e] = f16x2(y[2 * e], y[2 * e + 1]);
+                    tmem_st_u32(s_tm + 8 * c, w);  // over columns that have been read
                 }
-#pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    x[e] = ex2(fmaf(x[e], f, -off));
-                    l += x[e];
-                }
-#pragma unroll
-                for (int e = 0; e < 16; ++e) w[e] = f16x2(x[2 * e], x[2 * e + 1]);
-                tmem_st_u32(s_tm + c / 2, w);  // over columns that have been read
-            }
             tmem_st_wait();
             arrive(kBarP + st);
+            if (issues) {
+                if (!(ok = wait_for(kBarP + st, k & 1) && wait_for(kBarVt + st, k & 1))) break;
+                output(k > 0);
+                if (j + 2 < ntiles) {  // S over P, behind the product that reads it
+                    if (!(ok = wait_for(kBarK + st, (k + 1) & 1))) break;
+                    scores();
+                }
+            }
         }
         // Join the streams: the second's O comes through shared memory, once all products are done.
         if (ok) {
@@ -245,8 +286,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
             }
         } else if (ok) {
             if (ntiles > 1) ok = wait_for(kBarJoin, 0);
-            const int64_t unit = (((int64_t)b * a.kv.Hk + h) * a.tiles + tile) * a.splits + split;
-            const float inv = ns > 1 ? 1.f : sum == 0.f ? 0.f : a.kv.v_scale / sum;
+            const float inv = sum == 0.f ? 0.f : a.kv.v_scale / sum;
             if (ok) {
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
@@ -263,11 +303,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
                         const float w = snan[(c + e) >> 4] < seen ? NAN : inv;
                         x[e] = y.x * w; x[e + 1] = y.y * w; x[e + 2] = y.z * w; x[e + 3] = y.w * w;
                     }
-                    if (live && ns > 1) {
-                        float4 *dst = reinterpret_cast<float4 *>(a.part + (unit * 128 + row) * D + c);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) dst[e] = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
-                    } else if (live) {
+                    if (live) {
                         uint4 *dst = reinterpret_cast<uint4 *>(a.out + q_at + c);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
@@ -282,126 +318,126 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
                     }
                     __syncwarp();
                 }
-                if (live && ns > 1) {
-                    float2 *ml = reinterpret_cast<float2 *>(a.part + (int64_t)a.B * a.kv.Hk * a.tiles * a.splits * 128 * D);
-                    ml[unit * 128 + row] = make_float2(top, sum);
-                }
             }
         }
-    } else if (warp < kTilesIssuer) {
-        // Thread: a token of a tile.
-        const int row = tid - 32 * kWide0;
+        if (*sfail && issues) {  // products that may still run
+            if (lead) umma_commit(bar + kBarDrain + st);
+            __syncwarp();
+            bar_wait(bar + kBarDrain + st, 0);
+        }
+    } else {
+        // A warp has 16 tokens, 8 at a time: lane (token, quarter of its channels), so that a warp's read is one run of
+        // 8 D/2 bytes (a token a lane took 1800 cycles a tile in reads of 32 lines each) and 8 neighbouring lanes'
+        // writes of a chunk fall into different banks.
+        constexpr int W = D / 32;  // words of 8 codes in a quarter
+        const int tok = 16 * (warp - kWide0) + (lane & 7), quarter = lane >> 3;
         const int64_t head_bytes = kv4_head_bytes(ps, D);
         struct Bytes {
-            uint4 k[D / 32], v[D / 32];
-            uint32_t ks[D / 64], vs[D / 64];
-            bool gone;
+            uint32_t k[2][W], v[2][W], ks[2], vs[2];
+            uint32_t live, gone;  // bit u, of token tok + 8 u: to be read; to be read, but its page is not there
         };
-        auto fetch = [&](int j) {
+        // The page of a warp's tokens is looked up a tile before their bytes are fetched, and those a tile before they
+        // are widened.  Its place in the table and theirs in the page move on by a tile without a division.
+        struct Page {
+            int p, off;
+        };
+        const int step_pages = 128 / ps, step_off = 128 - step_pages * ps;
+        int left = t_end - 16 * (warp - kWide0);  // tokens from this warp's first on
+        int at = 16 * (warp - kWide0) / ps, off = 16 * (warp - kWide0) - at * ps;
+        const int32_t *table = a.table + (int64_t)b * a.max_pages;
+        auto page_of_next = [&] {
+            const Page x{left > 0 ? table[at] : 0, off};
+            at += step_pages;
+            off += step_off;
+            if (off >= ps) {
+                off -= ps;
+                ++at;
+            }
+            left -= 128;
+            return x;
+        };
+        const int64_t page_bytes = a.kv.Hk * head_bytes;
+        const uint8_t *head = a.cache + h * head_bytes;
+        const int in_code = (lane & 7) * (D / 2) + quarter * (D / 8), in_scale = ps * (D / 2) + (lane & 7) * (D / 16) + quarter * (D / 64);
+        // (Loads without a branch around them: one that joins a zero for what is not read waits for the load there.)
+        auto fetch = [&](int j, const Page &pg) {
             Bytes x;
+            x.live = x.gone = 0;
 #pragma unroll
-            for (int u = 0; u < D / 32; ++u) x.k[u] = x.v[u] = make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int u = 0; u < D / 64; ++u) x.ks[u] = x.vs[u] = 0;
-            x.gone = false;
-            const int t = t_begin + 128 * j + row;
-            if (j < ntiles && t < t_end) {
-                const int at = t / ps, off = t - at * ps, page = a.table[(int64_t)b * a.max_pages + at];
-                if (page < 0 || page >= a.kv.pages) {
-                    report_opt(a.err, DEV_BAD_PAGE, b, h, page);
-                    x.gone = true;
+            for (int u = 0; u < 2; ++u) {
+                const int page = pg.p;
+                const bool want = 128 * j + tok + 8 * u < t_end, there = page >= 0 && page < a.kv.pages;
+                x.live |= (uint32_t)(want && there) << u;
+                x.gone |= (uint32_t)(want && !there) << u;
+                const uint8_t *kp = head + (want && there ? page : 0) * page_bytes, *vp = kp + ps * (D * 9 / 16);
+                const int o = pg.off + 8 * u, code = in_code + o * (D / 2), sc = in_scale + o * (D / 16);
+                if constexpr (D == 128) {
+                    const uint4 kw = *reinterpret_cast<const uint4 *>(kp + code), vw = *reinterpret_cast<const uint4 *>(vp + code);
+                    x.k[u][0] = kw.x; x.k[u][1] = kw.y; x.k[u][2] = kw.z; x.k[u][3] = kw.w;
+                    x.v[u][0] = vw.x; x.v[u][1] = vw.y; x.v[u][2] = vw.z; x.v[u][3] = vw.w;
+                    x.ks[u] = *reinterpret_cast<const uint16_t *>(kp + sc);
+                    x.vs[u] = *reinterpret_cast<const uint16_t *>(vp + sc);
                 } else {
-                    const uint8_t *kp = a.cache + ((int64_t)page * a.kv.Hk + h) * head_bytes, *vp = kp + ps * (D * 9 / 16);
-                    const int code = off * (D / 2), sc = ps * (D / 2) + off * (D / 16);
-#pragma unroll
-                    for (int u = 0; u < D / 32; ++u) {
-                        x.k[u] = *reinterpret_cast<const uint4 *>(kp + code + 16 * u);
-                        x.v[u] = *reinterpret_cast<const uint4 *>(vp + code + 16 * u);
-                    }
-#pragma unroll
-                    for (int u = 0; u < D / 64; ++u) {
-                        x.ks[u] = *reinterpret_cast<const uint32_t *>(kp + sc + 4 * u);
-                        x.vs[u] = *reinterpret_cast<const uint32_t *>(vp + sc + 4 * u);
-                    }
+                    const uint2 kw = *reinterpret_cast<const uint2 *>(kp + code), vw = *reinterpret_cast<const uint2 *>(vp + code);
+                    x.k[u][0] = kw.x; x.k[u][1] = kw.y;
+                    x.v[u][0] = vw.x; x.v[u][1] = vw.y;
+                    x.ks[u] = kp[sc];
+                    x.vs[u] = vp[sc];
                 }
             }
             return x;
         };
-        auto put = [&](uint8_t *to, const uint4 (&codes)[D / 32], const uint32_t (&scales)[D / 64]) {
+        auto put = [&](uint8_t *to, const uint32_t (&codes)[2][W], const uint32_t (&scales)[2], uint32_t live) {
 #pragma unroll
-            for (int w = 0; w < D / 8; ++w) {  // words of 8 codes, two to a block
-                uint32_t hh[4];
-                widen((&codes[w >> 2].x)[w & 3], hh);
-                const uint32_t s2 = scales2((scales[w >> 3] >> (8 * ((w >> 1) & 3))) & 0xff), s = __byte_perm(s2, s2, 0x1010);
-                *reinterpret_cast<uint4 *>(to + sw128_chunk(row, w, 128)) = make_uint4(mul2(hh[0], s), mul2(hh[1], s), mul2(hh[2], s), mul2(hh[3], s));
+            for (int u = 0; u < 2; ++u) {
+                const uint32_t s2 = live >> u & 1 ? scales2(scales[u]) : 0;  // what is not there holds zeros
+#pragma unroll
+                for (int w = 0; w < W; ++w) {
+                    uint32_t hh[4];
+                    widen(codes[u][w], hh);
+                    const uint32_t s = __byte_perm(s2, s2, w < 2 ? 0x1010 : 0x3232);
+                    *reinterpret_cast<uint4 *>(to + sw128_chunk(tok + 8 * u, quarter * W + w, 128)) =
+                        make_uint4(mul2(hh[0], s), mul2(hh[1], s), mul2(hh[2], s), mul2(hh[3], s));
+                }
             }
         };
-        Bytes cur = fetch(0);
+        Page page = page_of_next();
+        Bytes cur = fetch(0, page);
+        page = page_of_next();
         for (int j = 0; j < ntiles; ++j) {
-            const int st = j & 1, k = j >> 1, t = t_begin + 128 * j + row;
-            const Bytes next = fetch(j + 1);
-            // A NaN value leaves the product (0 NaN is NaN); the first token with one is kept for its block.
-#pragma unroll
-            for (int u = 0; u < D / 16; ++u)
-                if (((cur.vs[u >> 2] >> (8 * (u & 3))) & 0x7f) == 0x7f) {
-                    atomicMin(snan + u, t);
-                    cur.vs[u >> 2] &= ~(0xffu << (8 * (u & 3)));
-                }
+            const int st = j & 1, k = j >> 1, t = 128 * j + tok;
+            const Bytes next = fetch(j + 1, page);
+            page = page_of_next();
             if (j >= 2 && !wait_for(kBarSc + st, (k - 1) & 1)) break;
-            const uint32_t gone = __ballot_sync(0xffffffffu, cur.gone);
-            if (lane == 0) sgone[4 * (j & 3) + warp - kWide0] = gone;
-            put(sm + L::kKt + st * L::kTileB, cur.k, cur.ks);
+            uint32_t gone = 0;  // bit of every token of the warp (its quarters agree)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) gone |= (__ballot_sync(0xffffffffu, cur.gone >> u & 1) & 0xff) << (8 * u);
+            if (lane == 0) {
+                reinterpret_cast<uint16_t *>(sgone)[8 * (j & 3) + warp - kWide0] = (uint16_t)gone;
+                if (gone) report_opt(a.err, DEV_BAD_PAGE, b, h, 128 * j);
+            }
+            put(sm + L::kKt + st * L::kTileB, cur.k, cur.ks, cur.live);
             fence_async_smem();
             arrive(kBarK + st);
+            // A NaN value leaves the product (0 NaN is NaN); the first token with one is kept for its block.
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int e = 0; e < D / 64; ++e)
+                    if ((cur.live >> u & 1) && ((cur.vs[u] >> (8 * e)) & 0x7f) == 0x7f) {
+                        atomicMin(snan + quarter * (D / 64) + e, t + 8 * u);
+                        cur.vs[u] &= ~(0xffu << (8 * e));
+                    }
             if (j >= 2 && !wait_for(kBarPv + st, (k - 1) & 1)) break;
-            put(sm + L::kVt + st * L::kTileB, cur.v, cur.vs);
+            put(sm + L::kVt + st * L::kTileB, cur.v, cur.vs, cur.live);
             fence_async_smem();
             arrive(kBarVt + st);
             cur = next;
         }
-    } else {
-        const bool lead = elect_one();
-        const uint32_t smem0 = smem_u32(sm), q = sw128_desc_lo(smem0 + L::kQ);
-        auto scores = [&](int j) {
-            const uint32_t kd = sw128_desc_lo(smem0 + L::kKt + (j & 1) * L::kTileB);
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) {
-                const uint32_t at = ((ks >> 2) * 128 * 128 + (ks & 3) * 32) / 16;
-                umma_bf16(tmem + 128 * (j & 1), sw128_desc_of(q + at), sw128_desc_of(kd + at), idesc_f16_f32(128, 128, false), ks > 0);
-            }
-            umma_commit(bar + kBarSc + (j & 1));
-        };
-        auto output = [&](int j) {
-            const uint32_t vd = sw128_desc_lo(smem0 + L::kVt + (j & 1) * L::kTileB, 128 * 128);
-#pragma unroll
-            for (int ks = 0; ks < 8; ++ks)
-                umma_ts(tmem + kTmO + D * (j & 1), tmem + 128 * (j & 1) + 8 * ks, sw128_desc_of(vd + ks * 2048 / 16),
-                        idesc_f16_f32(128, D, true), j > 1 || ks > 0);
-            umma_commit(bar + kBarPv + (j & 1));
-        };
-        bool ok = ntiles == 0 || wait_for(kBarQ, 0);
-        for (int j = 0; ok && j < 2 && j < ntiles; ++j) {
-            if (!(ok = wait_for(kBarK + j, 0))) break;
-            if (lead) scores(j);
-        }
-        for (int j = 0; ok && j < ntiles; ++j) {
-            const int st = j & 1, k = j >> 1;
-            if (!(ok = wait_for(kBarVt + st, k & 1) && wait_for(kBarP + st, k & 1))) break;
-            if (lead) output(j);
-            if (j + 2 < ntiles) {
-                if (!(ok = wait_for(kBarK + st, (k + 1) & 1))) break;
-                if (lead) scores(j + 2);
-            }
-        }
-        if (*sfail) {  // products that may still run
-            if (lead) umma_commit(bar + kBarDrain);
-            __syncwarp();
-            bar_wait(bar + kBarDrain, 0);
-        }
     }
     tc_fence_before();
     __syncthreads();
-    if (*sfail && tid == 0) report_opt(a.err, DEV_PIPE_TIMEOUT, b, h, t_begin);
+    if (*sfail && tid == 0) report_opt(a.err, DEV_PIPE_TIMEOUT, b, h, row0);
     if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
@@ -410,7 +446,7 @@ template <int D> cudaError_t launch(const AttendArgs &a, cudaStream_t st) {
     const int need = TilesSmem<D>::kBytes + 1024, smem = need > 116 * 1024 ? need : 116 * 1024;
     const cudaError_t e = cudaFuncSetAttribute(attend_tiles_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    attend_tiles_kernel<D><<<dim3(a.splits, a.tiles * a.kv.Hk, a.B), kTilesThreads, smem, st>>>(a);
+    attend_tiles_kernel<D><<<dim3(a.tiles, a.kv.Hk, a.B), kTilesThreads, smem, st>>>(a);
     return cudaGetLastError();
 }
 

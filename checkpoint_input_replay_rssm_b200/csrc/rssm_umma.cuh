@@ -148,21 +148,22 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
     for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
 }
 
-// The same into the upper half of a 64-value array or the lower, without waiting (tmem_ld_wait).
-template <int AT>
-__device__ __forceinline__ void tmem_ld32_at(uint32_t taddr, float (&v)[64]) {
+// 16 columns on their way: the values are there once tmem_ld_wait has been given them (which waits for every load
+// of this thread, so that the next one is started behind it).
+__device__ __forceinline__ void tmem_ld16_start(uint32_t taddr, float (&v)[16]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=f"(v[AT]), "=f"(v[AT + 1]), "=f"(v[AT + 2]), "=f"(v[AT + 3]), "=f"(v[AT + 4]), "=f"(v[AT + 5]),
-          "=f"(v[AT + 6]), "=f"(v[AT + 7]), "=f"(v[AT + 8]), "=f"(v[AT + 9]), "=f"(v[AT + 10]), "=f"(v[AT + 11]),
-          "=f"(v[AT + 12]), "=f"(v[AT + 13]), "=f"(v[AT + 14]), "=f"(v[AT + 15]), "=f"(v[AT + 16]), "=f"(v[AT + 17]),
-          "=f"(v[AT + 18]), "=f"(v[AT + 19]), "=f"(v[AT + 20]), "=f"(v[AT + 21]), "=f"(v[AT + 22]), "=f"(v[AT + 23]),
-          "=f"(v[AT + 24]), "=f"(v[AT + 25]), "=f"(v[AT + 26]), "=f"(v[AT + 27]), "=f"(v[AT + 28]), "=f"(v[AT + 29]),
-          "=f"(v[AT + 30]), "=f"(v[AT + 31])
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+          "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
         : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_ld_wait(float (&v)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                   "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
+                 :
+                 : "memory");
+}
 
 // Store 32 consecutive fp32 columns of this thread's lane.  Waits for the store.
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32]) {
