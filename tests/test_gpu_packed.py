@@ -461,6 +461,49 @@ def test_attend_nan_stays_with_the_rows_that_see_it():
     assert torch.equal(err, _err())
 
 
+@pytest.mark.parametrize("D,ps", [(128, 16), (64, 48), (128, 256)])
+def test_attend_prompt_chunks_with_nan_bad_pages_and_rows_that_see_nothing(D, ps):
+    """The same with enough rows for the tiles of 128: a NaN value and a NaN key at token 150 stay with the rows behind
+    it, a page that is not there is left out, more rows than cached tokens leave the first ones 0."""
+    lens, news = [200, 30, 300], [150, 40, 129]
+    c = _attend_case(D + ps, lens, news, 16, 1, D, ps, pad=3, first=2)
+    clean = _attend_run(c)
+    _attend_check(c, clean)
+    assert not clean[152:162].any()  # the second request's first rows
+    row0, g = c["cu"][0], 16
+    page, off = c["table"][0, 150 // ps].item(), 150 % ps
+    rows = np.arange(150)
+    seen = rows + 200 - 150 + 1 > 150
+    for is_v in (True, False):
+        at = (ps * D * 9 // 16 if is_v else 0) + ps * D // 2 + off * (D // 16) + 2
+        kept = c["cache"][page, 0, at].item()
+        c["cache"][page, 0, at] = 0x7F
+        err = _err()
+        got = _np(rssm.kv4_attend(c["q"], c["cache"], c["table"], c["lens"], _i(c["cu"]), c["max_q"], err=err, **c["kw"]))
+        c["cache"][page, 0, at] = kept
+        assert err.tolist() == [0, 0, 0, 0]
+        mine, ref = got[row0:row0 + 150], clean[row0:row0 + 150]
+        assert np.array_equal(mine[~seen], ref[~seen])
+        assert np.isnan(mine[seen][:, :, 32:48] if is_v else mine[seen]).all()
+        if is_v:
+            assert np.array_equal(np.delete(mine[seen], np.arange(32, 48), 2), np.delete(ref[seen], np.arange(32, 48), 2))
+        assert np.array_equal(got[row0 + 150:c["cu"][-1]], clean[row0 + 150:c["cu"][-1]])
+    table = c["table"].clone()
+    table[2, 0] = c["cache"].shape[0]
+    err = _err()
+    got = _np(rssm.kv4_attend(c["q"], c["cache"], table, c["lens"], _i(c["cu"]), c["max_q"], err=err, **c["kw"]))
+    assert err[:2].tolist() == [rssm.RSSM_DEV_BAD_PAGE, 2]
+    assert np.array_equal(got[row0:c["cu"][2]], clean[row0:c["cu"][2]])
+    q, cut = c["q"][c["cu"][2]:c["cu"][3]], min(ps, 300)
+    want = []
+    for i in range(129):  # row by row: what is left out lies before what is seen
+        n = 300 - 129 + i + 1
+        want.append(packed.attend(_np(q[i:i + 1]), [c["K"][2][cut:n]], [c["V"][2][cut:n]], [0, 1], D ** -0.5)[0][0])
+    far = np.abs(got[c["cu"][2]:c["cu"][3]] - np.array(want))
+    assert far.max() <= 2.0 ** -7 * np.abs(c["V"][2]).max()  # bf16 output and fp16 weights, in the largest value
+    assert g == 16
+
+
 def test_attend_bad_lengths_and_pages_are_reported():
     import torch
 
