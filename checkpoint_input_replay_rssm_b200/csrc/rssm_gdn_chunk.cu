@@ -87,8 +87,6 @@ __global__ void __launch_bounds__(kChunkThreads, 4) gdn_chunk_kernel(const GdnPr
     int *sfound = reinterpret_cast<int *>(bar + 2);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int slot = blockIdx.x, h = blockIdx.y, H = a.H;
-    pdl_trigger();  // the scan's CTAs may start: they read this kernel's results behind their own wait
-
     // The request of this slot: the last b with cu[b] / 64 + b <= slot, 32 candidates a round.
     if (warp == 0) {
         int lo = 0, n = a.B;  // b is in [lo, lo + n)
@@ -110,6 +108,9 @@ __global__ void __launch_bounds__(kChunkThreads, 4) gdn_chunk_kernel(const GdnPr
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    // The scan's CTAs may start (they read this kernel's results behind their own wait), once this one has its tensor
+    // memory: one of them has all of an SM's.
+    pdl_trigger();
     const uint32_t tmem = *tslot;
     const int b = *sfound;
     int r0, r1;

@@ -6,14 +6,17 @@
 // state's rows are independent (row p meets only v[p]), so a warp owns 8 of them and
 // keeps them in registers over the whole prompt.  Per token and row s:
 //   a = alpha s,  c = beta (v[p] - a . k),  o[p] = a . q + c (k . q),  s = a + c k
-// The output is written from the decayed old state, so that the three dot products
-// a.k, a.q, k.q are one reduction (8 lanes, 3 shuffles) instead of two in sequence:
-// the chain through the reduction bounds this kernel, not HBM.  A row's columns lie
-// over 8 lanes in float4 pieces, 4 lane groups of 2 rows each.  Tokens are staged 16 at
-// a time in shared memory (fp32), the next 16 in flight meanwhile.
+// The output is written from the decayed old state, so that the dot products a.k and a.q
+// are one reduction (8 lanes, 3 shuffles) instead of two in sequence, and k.q is formed
+// once per token for all rows: the issue of a token's instructions and the chain through
+// the reduction bound this kernel, not HBM.  A row's columns lie over 8 lanes in pieces
+// of 16 bytes, 4 lane groups of 2 rows each; products take two columns an instruction
+// (fp32 pairs).  Tokens are staged 16 at a time in shared memory (fp32), the next 16 in
+// flight meanwhile.
 #include "rssm_gdn_prefill.h"
 #include "rssm_internal.h"
 #include "rssm_packed.cuh"
+#include "rssm_pair.cuh"
 
 namespace rssm {
 
@@ -34,9 +37,11 @@ __global__ void __launch_bounds__(32 * kRecWarps) gdn_recurrent_kernel(const Gdn
     constexpr int kThr = 32 * kRecWarps;
     constexpr int V = N >= 32 ? 4 : 2;  // columns per piece
     constexpr int J = N / (8 * V);      // pieces per lane
+    constexpr int U = J * V / 2;        // pairs per lane and row
     constexpr int NQ = kRecTok * N / kThr, NV = kRecTok * kRecRows / kThr;
+    typedef unsigned long long u64;
     __shared__ __align__(16) float sk[2][kRecTok][N], sq[2][kRecTok][N];
-    __shared__ float sv[2][kRecTok][kRecRows], sa[2][kRecTok], sb[2][kRecTok];
+    __shared__ float sv[2][kRecTok][kRecRows], sa[2][kRecTok], sb[2][kRecTok], skq[kRecTok];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int l8 = lane & 7, g4 = lane >> 3;
     const int h = blockIdx.y, b = blockIdx.z, p0 = blockIdx.x * kRecRows;
@@ -49,14 +54,27 @@ __global__ void __launch_bounds__(32 * kRecWarps) gdn_recurrent_kernel(const Gdn
     const int64_t head = (int64_t)b * a.H + h;
     const int row0 = 8 * warp + 2 * g4;  // this lane group's rows: row0, row0 + 1 (P is a multiple of 8)
     const bool on = row0 < rows;
-    float s[2][J][V];
+    // This lane's pairs of a row of N values: V consecutive ones of every 8 V.
+    auto pairs = [&](const float *row, u64 (&x)[U]) {
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
+        for (int j = 0; j < J; ++j) {
+            const float *at = row + j * 8 * V + l8 * V;
+            if constexpr (V == 4) {
+                const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(at);
+                x[2 * j] = v.x;
+                x[2 * j + 1] = v.y;
+            } else {
+                x[j] = *reinterpret_cast<const u64 *>(at);
+            }
+        }
+    };
+    u64 s[2][U];
 #pragma unroll
-        for (int j = 0; j < J; ++j)
+    for (int r = 0; r < 2; ++r) {
 #pragma unroll
-            for (int e = 0; e < V; ++e)
-                s[r][j][e] = on && a.S0 ? a.S0[(head * a.P + p0 + row0 + r) * N + j * 8 * V + l8 * V + e] : 0.f;
+        for (int u = 0; u < U; ++u) s[r][u] = 0;
+        if (on && a.S0) pairs(a.S0 + (head * a.P + p0 + row0 + r) * N, s[r]);
+    }
 
     float rk[NQ], rq[NQ], rv[NV], ra = 0.f, rb = 0.f;
     auto fetch = [&](int t0) {
@@ -104,42 +122,61 @@ __global__ void __launch_bounds__(32 * kRecWarps) gdn_recurrent_kernel(const Gdn
         __syncthreads();
         if (t0 + kRecTok < r1) fetch(t0 + kRecTok);
         const int nt = min(kRecTok, r1 - t0);
+        // k . q of every token, 8 lanes a token: once for all of the CTA's rows
+        {
+            const int t = 4 * warp + g4;
+            u64 kk[U], qq[U], d2 = 0;
+            pairs(sk[buf][t], kk);
+            pairs(sq[buf][t], qq);
+#pragma unroll
+            for (int u = 0; u < U; ++u) d2 = f2_fma(kk[u], qq[u], d2);
+            float lo, hi;
+            f2_unpack(d2, lo, hi);
+            lo += hi;
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) lo += __shfl_xor_sync(0xffffffffu, lo, o);
+            if (l8 == 0) skq[t] = lo;
+        }
+        __syncthreads();
+#pragma unroll 2
         for (int t = 0; t < nt; ++t) {
-            const float al = sa[buf][t];
-            float dk[2] = {0.f, 0.f}, dq[2] = {0.f, 0.f}, kq = 0.f, kv[J][V];
+            const float al = sa[buf][t], be = sb[buf][t], kq = skq[t];
+            const u64 al2 = f2_pack(al, al);
+            u64 kk[U], qq[U], dk2[2] = {0, 0}, dq2[2] = {0, 0};
+            pairs(sk[buf][t], kk);
+            pairs(sq[buf][t], qq);
 #pragma unroll
-            for (int j = 0; j < J; ++j)
+            for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    const float kk = sk[buf][t][j * 8 * V + l8 * V + e], qq = sq[buf][t][j * 8 * V + l8 * V + e];
-                    kv[j][e] = kk;
-                    kq = fmaf(kk, qq, kq);
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        s[r][j][e] *= al;
-                        dk[r] = fmaf(s[r][j][e], kk, dk[r]);
-                        dq[r] = fmaf(s[r][j][e], qq, dq[r]);
-                    }
+                for (int r = 0; r < 2; ++r) {
+                    s[r][u] = f2_mul(s[r][u], al2);
+                    dk2[r] = f2_fma(s[r][u], kk[u], dk2[r]);
+                    dq2[r] = f2_fma(s[r][u], qq[u], dq2[r]);
                 }
+            float dk[2], dq[2];
 #pragma unroll
-            for (int o = 1; o < 8; o <<= 1) {
-                kq += __shfl_xor_sync(0xffffffffu, kq, o);
+            for (int r = 0; r < 2; ++r) {
+                float lo, hi;
+                f2_unpack(dk2[r], lo, hi);
+                dk[r] = lo + hi;
+                f2_unpack(dq2[r], lo, hi);
+                dq[r] = lo + hi;
+            }
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1)
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     dk[r] += __shfl_xor_sync(0xffffffffu, dk[r], o);
                     dq[r] += __shfl_xor_sync(0xffffffffu, dq[r], o);
                 }
-            }
-            const float be = sb[buf][t];
             float o[2];
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 const float c = be * (sv[buf][t][row0 + r] - dk[r]);
+                const u64 c2 = f2_pack(c, c);
                 o[r] = fmaf(c, kq, dq[r]);
 #pragma unroll
-                for (int j = 0; j < J; ++j)
-#pragma unroll
-                    for (int e = 0; e < V; ++e) s[r][j][e] = fmaf(c, kv[j][e], s[r][j][e]);
+                for (int u = 0; u < U; ++u) s[r][u] = f2_fma(c2, kk[u], s[r][u]);
             }
             if (l8 == 0 && on)
                 *reinterpret_cast<float2 *>(a.y + ((int64_t)(t0 + t) * a.H + h) * a.P + p0 + row0) =
@@ -150,10 +187,10 @@ __global__ void __launch_bounds__(32 * kRecWarps) gdn_recurrent_kernel(const Gdn
 #pragma unroll
         for (int r = 0; r < 2; ++r)
 #pragma unroll
-            for (int j = 0; j < J; ++j)
-#pragma unroll
-                for (int e = 0; e < V; ++e)
-                    a.S_out[(head * a.P + p0 + row0 + r) * N + j * 8 * V + l8 * V + e] = s[r][j][e];
+            for (int u = 0; u < U; ++u) {
+                const int at = V == 4 ? (u >> 1) * 32 + l8 * 4 + 2 * (u & 1) : u * 16 + l8 * 2;
+                *reinterpret_cast<u64 *>(a.S_out + (head * a.P + p0 + row0 + r) * N + at) = s[r][u];
+            }
 }
 
 template <typename IN>

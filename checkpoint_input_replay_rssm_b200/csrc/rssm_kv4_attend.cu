@@ -548,6 +548,7 @@ bool attend_plan(const rssm_kv4_config *c, const rssm_attend_config *t, Kv4Args 
     if (p->mt != 8 && tiles * kv->Hk > 65535) return false;
     int64_t seq = (int64_t)t->max_pages * kv->ps;
     if (t->max_seq < seq) seq = t->max_seq;
+    if (seq > 1 << 30) return false;  // positions and their strides are int32
     // Tokens of one CTA: a share of the work that fills the machine (148 SMs, 3 CTAs each) kWaves times over,
     // between 256 (a shorter one is all start and join) and kMaxL (a longer one makes a long tail).
     const int64_t units = (int64_t)t->batch * kv->Hk * tiles, want = 148 * 3 * kWaves;

@@ -170,7 +170,7 @@ extern "C" RSSM_API rssm_status rssm_build_tables(const rssm_tables_config *cfg,
                                                   int32_t *next_free, int32_t *dev_error, void *stream) {
     using namespace rssm;
     if (!cfg || !cached_len || !new_len || !free_head || !block_table || !cu_new || !seq_len || !slot_map ||
-        !position || !next_free || next_free == free_head)
+        !position || !next_free || next_free == free_head || seq_len == cached_len || seq_len == new_len)
         return RSSM_EINVAL;
     const rssm_tables_config &c = *cfg;
     if (c.batch < 1 || c.batch > kMaxRequests || c.page_size < 1 || c.page_size > 65536 || c.max_pages < 1 ||

@@ -307,7 +307,7 @@ RSSM_API rssm_status rssm_gdn_prefill(const rssm_gdn_prefill_config *cfg, const 
  *               num_free = entries of free_pages; max_tokens = rows of slot_map and position
  *               (both at most 2^30).
  *   cu_new:     int32[B+1] packed offsets of the new tokens.
- *   seq_len:    int32[B] cached_len + new_len.
+ *   seq_len:    int32[B] cached_len + new_len (may not alias either: every CTA reads them).
  *   slot_map:   int32[max_tokens] slot of every new token, page * page_size + offset.
  *   position:   int32[max_tokens] its position in its request.  Rows behind the last new
  *               token hold -1 in both.
@@ -343,7 +343,7 @@ typedef struct {
 /* Bytes of the cache (0 if cfg is invalid). */
 RSSM_API size_t rssm_kv4_cache_bytes(const rssm_kv4_config *cfg);
 
-/* Write `tokens` rows of k and v (device bf16 [tokens][n_kv_heads][head_dim]) to the slots
+/* Write `tokens` >= 1 rows of k and v (device bf16 [tokens][n_kv_heads][head_dim]) to the slots
  * slot_map[t].  A negative slot is skipped; one past the cache sets RSSM_DEV_BAD_PAGE.  Slots
  * of one call are distinct (of two rows with one slot, either or a mixture of blocks stays). */
 RSSM_API rssm_status rssm_kv4_append(const rssm_kv4_config *cfg, int32_t tokens, const void *k, const void *v,
@@ -361,7 +361,7 @@ RSSM_API rssm_status rssm_kv4_export(const rssm_kv4_config *cfg, int32_t tokens,
  *   batch 1..65535, n_q_heads a multiple of n_kv_heads, tokens = rows of q and out,
  *   max_pages = row length of block_table (int32 [B][max_pages]), max_q >= every n,
  *   max_seq >= every seq_len (both size the launch, so that it can be captured once for
- *   growing requests).  q, out: device bf16 [tokens][n_q_heads][head_dim]; rows of no request
+ *   growing requests; the lesser of max_seq and max_pages * page_size is at most 2^30).  q, out: device bf16 [tokens][n_q_heads][head_dim]; rows of no request
  *   are left as they were.
  *   workspace: device, 256-byte aligned, rssm_kv4_attend_workspace_bytes bytes (NULL where 0).
  * A request whose offsets or length do not fit (cu_q out of order or past tokens, n > max_q,

@@ -95,18 +95,19 @@ TAB = ("cached_len", "new_len", "free_pages", "free_head", "block_table", "cu_ne
        "next_free")
 
 
-def _tables(drop=(), alias=False, **kw):
+def _tables(drop=(), alias=None, **kw):
     c = dict(batch=2, page_size=16, max_pages=4, num_free=8, max_tokens=32) | kw
     p = [None if n in drop else P16 * (i + 1) for i, n in enumerate(TAB)]
     if alias:
-        p[9] = p[3]
+        p[TAB.index(alias[0])] = p[TAB.index(alias[1])]
     cfg = rssm.rssm_tables_config(*c.values())
     return rssm.load().rssm_build_tables(ctypes.byref(cfg), *p, None, None)
 
 
 @pytest.mark.parametrize("kw", [
     dict(batch=0), dict(batch=16385), dict(page_size=0), dict(page_size=65537), dict(max_pages=0), dict(num_free=-1),
-    dict(num_free=(1 << 30) + 1), dict(max_tokens=0), dict(max_tokens=(1 << 30) + 1), dict(alias=True),
+    dict(num_free=(1 << 30) + 1), dict(max_tokens=0), dict(max_tokens=(1 << 30) + 1), dict(alias=("next_free", "free_head")),
+    dict(alias=("seq_len", "cached_len")), dict(alias=("seq_len", "new_len")),
     dict(max_pages=1 << 20, page_size=4096)] + [dict(drop=(n,)) for n in TAB])
 def test_build_tables_refuses(kw):
     assert _tables(**kw) == rssm.RSSM_EINVAL
@@ -169,7 +170,7 @@ def _attend(cfg=None, null=None, off=None, ws=P16, ws_bytes=1 << 40, **kw):
 
 @pytest.mark.parametrize("kw", [
     dict(batch=0), dict(batch=65536), dict(n_q_heads=0), dict(n_q_heads=7), dict(n_q_heads=65536), dict(tokens=0),
-    dict(max_pages=0), dict(max_q=0), dict(max_seq=0), dict(sm_scale=float("nan")), dict(sm_scale=float("inf"))]
+    dict(max_pages=0), dict(max_q=0), dict(max_seq=0), dict(max_pages=1 << 27, max_seq=(1 << 30) + 1), dict(sm_scale=float("nan")), dict(sm_scale=float("inf"))]
     + [dict(null=i) for i in range(6)] + [dict(off=i) for i in (0, 1, 5)])
 def test_attend_refuses(kw):
     assert _attend(**kw) == rssm.RSSM_EINVAL
