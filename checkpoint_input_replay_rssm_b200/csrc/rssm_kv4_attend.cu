@@ -95,6 +95,17 @@ __global__ void __launch_bounds__(32 * kWarps4, MT == 1 ? 3 : 2) attend_kernel(c
     float *sf = reinterpret_cast<float *>(sm + S::kRow);
     int *sseen = reinterpret_cast<int *>(sm + S::kRow) + RT;
 
+    // Query operands, [mt][k-step][lane]: warp w makes those of the rows g + 8 (w & 1) of 16-row tile w >> 1.  Its rows
+    // are on their way while the page table is.
+    const int mt = warp >> 1, u = warp & 1, row = row0 + 16 * mt + g + 8 * u;
+    const bool live = row < rows;
+    const int i = live ? row / G : 0, hd = live ? row - i * G : 0;
+    const uint4 *src =
+        reinterpret_cast<const uint4 *>(a.q + ((int64_t)(r0 + i) * a.Hq + h * G + hd) * D + c * (D / 4));
+    uint4 raw[D / 32];
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) raw[k] = warp < 2 * MT && live ? src[k] : make_uint4(0, 0, 0, 0);
+
     // This warp's steps: tokens t_begin + 32 (warp + kWarps4 i).  Lane l keeps the page of
     // 16-token group l & 1 of step l >> 1 of a window of 16 steps, -1 for one that is not
     // read (behind the last token, or outside the cache).
@@ -156,18 +167,10 @@ __global__ void __launch_bounds__(32 * kWarps4, MT == 1 ? 3 : 2) attend_kernel(c
         cp_async_commit();
     }
 
-    // Query operands, [mt][k-step][lane]: warp w makes those of the rows g + 8 (w & 1) of 16-row tile w >> 1.
     if (warp < 2 * MT) {
-        const int mt = warp >> 1, u = warp & 1, row = row0 + 16 * mt + g + 8 * u;
-        const bool live = row < rows;
-        const int i = live ? row / G : 0, hd = live ? row - i * G : 0;
-        const uint4 *src =
-            reinterpret_cast<const uint4 *>(a.q + ((int64_t)(r0 + i) * a.Hq + h * G + hd) * D + c * (D / 4));
-        uint4 raw[D / 32];
         float top = 0.f;
 #pragma unroll
         for (int k = 0; k < D / 32; ++k) {
-            raw[k] = live ? src[k] : make_uint4(0, 0, 0, 0);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const uint32_t x = (&raw[k].x)[e];
@@ -485,11 +488,20 @@ __global__ void __launch_bounds__(32 * kWarps4, MT == 1 ? 3 : 2) attend_kernel(c
     }
 }
 
-// Join the splits of one tile: out = sum_s 2^{m_s - m} O_s / sum_s 2^{m_s - m} l_s.
+// Join the splits of a tile's rows: out = sum_s 2^{m_s - m} O_s / sum_s 2^{m_s - m} l_s.  D / 4 threads have a row, or,
+// where there are few tiles and many splits, two such groups with every second split each, and each group of rows a
+// CTA of its own (in sequence by one group, 79 splits of a long context took longer than the attention itself).
+template <int D, int MT> struct Join {
+    static constexpr int kThreads = 256, kLanes = D / 4;
+};
 template <int D, int MT>
-__global__ void __launch_bounds__(256) attend_join_kernel(const AttendArgs a) {
-    constexpr int RT = 16 * MT, TPR = D / 4;  // threads a row, 4 channels each
-    const int tile = blockIdx.x % a.tiles, h = blockIdx.x / a.tiles, b = blockIdx.y;
+__global__ void __launch_bounds__(Join<D, MT>::kThreads) attend_join_kernel(const AttendArgs a) {
+    using J = Join<D, MT>;
+    constexpr int RT = 16 * MT;
+    __shared__ float4 part[J::kThreads / 2];
+    const int at_once = gridDim.x / (a.tiles * a.kv.Hk), th = blockIdx.x / at_once, halves = at_once > 1 ? 2 : 1;
+    const int at_a_time = J::kThreads / (halves * J::kLanes);  // rows
+    const int tile = th % a.tiles, h = th / a.tiles, b = blockIdx.y;
     pdl_wait();  // first of all: no CTA ends before the kernel whose results it joins
     int r0, n, len;
     if (!attend_request(a, b, r0, n, len)) return;  // reported by the first kernel
@@ -498,26 +510,45 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttendArgs a) {
     const int last = min(row0 + RT, rows) - 1;
     const int ns = (max(0, len - n + last / a.G + 1) + a.L - 1) / a.L;
     if (ns <= 1) return;
+    const int l = threadIdx.x % J::kLanes, half = threadIdx.x / J::kLanes % halves, rl = threadIdx.x / (halves * J::kLanes);
     const int64_t unit = (((int64_t)b * a.kv.Hk + h) * a.tiles + tile) * a.splits;
-    const float2 *ml = reinterpret_cast<const float2 *>(a.part + (int64_t)a.B * a.kv.Hk * a.tiles * a.splits * RT * D);
-    for (int r = threadIdx.x / TPR; r < min(RT, rows - row0); r += 256 / TPR) {
-        const int at = (threadIdx.x % TPR) * 4;
+    const float2 *ml0 = reinterpret_cast<const float2 *>(a.part + (int64_t)a.B * a.kv.Hk * a.tiles * a.splits * RT * D) + unit * RT;
+    for (int r1st = blockIdx.x % at_once * at_a_time; r1st < RT; r1st += at_once * at_a_time) {
+        const int r = r1st + rl;
+        const float2 *ml = ml0 + r;
         float top = -INFINITY, sum = 0.f;
-#pragma unroll 4
-        for (int s = 0; s < ns; ++s) top = fmaxf(top, ml[(unit + s) * RT + r].x);
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int s = 0; s < ns; ++s) {
-            const float2 v = ml[(unit + s) * RT + r];
-            const float fac = v.x == -INFINITY ? 1.f : ex2(v.x - top);
-            const float4 x = *reinterpret_cast<const float4 *>(a.part + ((unit + s) * RT + r) * D + at);
-            sum += v.y * fac;
-            acc.x += x.x * fac; acc.y += x.y * fac; acc.z += x.z * fac; acc.w += x.w * fac;
+        for (int s = l; s < ns; s += J::kLanes) top = fmaxf(top, ml[s * RT].x);
+#pragma unroll
+        for (int o = 1; o < J::kLanes; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        for (int s = l; s < ns; s += J::kLanes) {
+            const float2 v = ml[s * RT];
+            sum += v.x == -INFINITY ? v.y : v.y * ex2(v.x - top);
         }
-        const float inv = sum == 0.f ? 0.f : a.kv.v_scale / sum;
-        const int i = (row0 + r) / a.G, hd = row0 + r - i * a.G;
-        const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-        *reinterpret_cast<uint2 *>(a.out + ((int64_t)(r0 + i) * a.Hq + h * a.G + hd) * D + at) =
-            make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+#pragma unroll
+        for (int o = 1; o < J::kLanes; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        const float *src = a.part + (unit * RT + r) * D + 4 * l;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int s = half; s < ns; s += halves) {
+            const float m = ml[s * RT].x, fac = m == -INFINITY ? 1.f : ex2(m - top);
+            const float4 x = *reinterpret_cast<const float4 *>(src + (int64_t)s * RT * D);
+            acc.x = fmaf(x.x, fac, acc.x); acc.y = fmaf(x.y, fac, acc.y); acc.z = fmaf(x.z, fac, acc.z); acc.w = fmaf(x.w, fac, acc.w);
+        }
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (halves == 2) {
+            if (half) part[rl * J::kLanes + l] = acc;
+            __syncthreads();
+            x = part[rl * J::kLanes + l];
+            __syncthreads();
+        }
+        if (!half && row0 + r < rows) {
+            const float inv = sum == 0.f ? 0.f : a.kv.v_scale / sum;
+            const int i = (row0 + r) / a.G, hd = row0 + r - i * a.G;
+            const __nv_bfloat162 lo = __floats2bfloat162_rn((acc.x + x.x) * inv, (acc.y + x.y) * inv);
+            const __nv_bfloat162 hi = __floats2bfloat162_rn((acc.z + x.z) * inv, (acc.w + x.w) * inv);
+            *reinterpret_cast<uint2 *>(a.out + ((int64_t)(r0 + i) * a.Hq + h * a.G + hd) * D + 4 * l) =
+                make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+        }
     }
 }
 
@@ -574,8 +605,11 @@ cudaError_t attend_launch(const AttendArgs &a, cudaStream_t st) {
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(a.tiles * a.kv.Hk, a.B);
-    cfg.blockDim = dim3(256);
+    // (one request over 4096 / 20000 tokens: 12.5 / 25 us against 18.6 / 50 with one CTA a tile; 256 requests: 116
+    // against 119 the other way about)
+    const bool few = (int64_t)a.B * a.tiles * a.kv.Hk < 148;
+    cfg.gridDim = dim3(a.tiles * a.kv.Hk * (few ? 16 * MT * 2 * Join<D, MT>::kLanes / Join<D, MT>::kThreads : 1), a.B);
+    cfg.blockDim = dim3(Join<D, MT>::kThreads);
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
