@@ -291,6 +291,27 @@ def test_cache_holds_the_nearest_values(T, Hk, D, ps, ke, ve):
     assert guard.shape == cache.shape
 
 
+@pytest.mark.parametrize("e", [0, -7, 60])
+def test_cache_codes_of_every_quotient(e):
+    """Every 8-bit value as a block's largest, so that every scale occurs, and every 8-bit value of
+    ten binades below it, so that every code and every border between two is met, exactly."""
+    import torch
+
+    m = np.arange(128, 256)
+    rest = np.concatenate([m * 2.0 ** -j for j in range(10)])
+    rest = np.concatenate([rest, -rest, np.zeros(-2 * len(rest) % 15)]).reshape(-1, 15)
+    top = np.repeat(m * 1.0, len(rest))[:, None]
+    x = np.concatenate([top, np.minimum(np.tile(rest, (128, 1)), top)], 1).reshape(-1, 2, 64) * 2.0 ** (e - 4)
+    k = _t(x, "bfloat16")
+    assert np.array_equal(_np(k), x)
+    cache = rssm.kv4_cache(-(-len(x) // 32), 2, 32, 64)
+    slots = _i(range(len(x)))
+    kw = dict(k_scale=2.0 ** e, v_scale=2.0 ** (e - 2))
+    rssm.kv4_append(k, k, slots, cache, **kw)
+    gk, gv = (_np(t) for t in rssm.kv4_export(slots, cache, 64, **kw))
+    assert np.array_equal(gk, packed.hold(x, 2.0 ** e)) and np.array_equal(gv, packed.hold(x, 2.0 ** (e - 2)))
+
+
 def test_cache_keeps_infinities_finite_and_nan_as_nan():
     import torch
 
