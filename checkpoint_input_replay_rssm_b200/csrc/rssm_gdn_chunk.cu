@@ -14,7 +14,7 @@
 //   R^T [T b; M T b]^T  (128 x 128 x 64: the K columns give U, the Q columns the second part of O)
 //   (w U)^T K        (128 x 128 x 64 onto the state, which stays in tensor memory)
 // q, k and v are bf16 and enter exactly; fp32 operands enter as a (hi, lo) bf16 pair, which
-// leaves 2^-17 of the value, and the lo lo product is dropped (2^-18): near-fp32 accuracy at
+// leaves 2^-18 of the value, and the lo lo product is dropped (2^-18): near-fp32 accuracy at
 // two or three bf16 products, where one tf32 product would leave 2^-11.
 //
 // T comes from forward substitution in fp32, in blocks: the 16 x 16 diagonal blocks
@@ -25,6 +25,13 @@
 //
 // Request b's chunk c has slot r0 / 64 + b + c (r0 its first row): slots do not collide, since
 // floor((x + len) / 64) + 1 >= ceil(len / 64), and no prefix sum over the requests is needed.
+//
+// 64 prompts of 1 to 1024 tokens (34500 in all), 32 heads, P = 128: 394 us for the chunk kernel and 472 for the
+// scan, of 259 at the rate of a copy for both (together 2.0 TB/s of what a call has to move).  The chunk kernel is
+// bound by the issue of its fp32 work in shared memory (1.7 instructions a cycle at four CTAs an SM, which its
+// shared memory and registers allow).  The scan is a chain: 2.6 us a chunk of a prompt, three products that wait
+// for each other and the conversions between them, with one CTA an SM, and about 13 us to start and end a CTA.  One
+// prompt of 8191 tokens: 94 and 330 us.
 #include <cuda_bf16.h>
 
 #include "rssm_gdn_prefill.h"

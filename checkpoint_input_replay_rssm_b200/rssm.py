@@ -325,6 +325,13 @@ def _cuda_index(t, name):
     return t.get_device()
 
 
+def _int(name, v):
+    """A size that reaches the library as int32, where a larger one would wrap."""
+    if not 0 <= v <= 0x7fffffff:
+        raise ValueError(f"{name}: expected a size below 2^31, got {v}")
+    return v
+
+
 def _ok(st, what):
     if st != RSSM_OK:
         raise RssmError(st, f"{what} refused its arguments" if st == RSSM_EINVAL else f"{what}: launch failed")
@@ -379,15 +386,15 @@ def build_tables(cached_len, new_len, free_pages, free_head, block_table, page_s
     if cached_len.dim() != 1 or block_table.dim() != 2 or free_pages.dim() != 1:
         raise ValueError("expected cached_len [requests], block_table [requests, pages] and free_pages [pages]")
     Bn, width = block_table.shape
-    if max_tokens < 1:
-        raise ValueError(f"max_tokens: expected at least 1, got {max_tokens}")
+    if max_tokens < 1 or max_tokens > 2 ** 30:
+        raise ValueError(f"max_tokens: expected 1 to 2^30, got {max_tokens}")
     sizes, out = (Bn + 1, Bn, max_tokens, max_tokens, 1), None
 
     def call(st):
         nonlocal out
         out = torch.empty(2 * Bn + 2 * max_tokens + 2, dtype=i32, device=cached_len.device).split_with_sizes(sizes)  # one allocation
         base = out[0].data_ptr()
-        cfg = rssm_tables_config(Bn, page_size, width, free_pages.shape[0], max_tokens)
+        cfg = rssm_tables_config(Bn, _int("page_size", page_size), width, _int("free_pages", free_pages.shape[0]), max_tokens)
         return load().rssm_build_tables(
             ctypes.byref(cfg), _want("cached_len", cached_len, i32, (Bn,), dev), _want("new_len", new_len, i32, (Bn,), dev),
             _want("free_pages", free_pages, i32, (free_pages.shape[0],), dev), _want("free_head", free_head, i32, (1,), dev),
@@ -415,6 +422,8 @@ def _kv4_config(cache, head_dim, k_scale, v_scale):
     if cache.dtype != torch.uint8 or cache.dim() != 3 or not cache.is_cuda or not cache.is_contiguous():
         raise ValueError("cache: expected a contiguous CUDA uint8 tensor [pages, kv heads, page bytes]")
     pages, heads, nb = cache.shape
+    if head_dim < 1:
+        raise ValueError(f"head_dim: expected 64 or 128, got {head_dim}")
     ps = nb * 8 // (9 * head_dim)
     if ps * 9 * head_dim != nb * 8:
         raise ValueError(f"cache: {nb} bytes a page and head are no whole number of tokens of {head_dim} channels")
@@ -487,7 +496,8 @@ def kv4_attend(q, cache, block_table, seq_len, cu_q, max_q, k_scale=1.0, v_scale
         nonlocal out
         out = torch.empty((T, Hq, D), dtype=bf, device=q.device) if out is None else out
         lib, kv = load(), ctypes.byref(cfg)
-        att = ctypes.byref(rssm_attend_config(Bn, Hq, T, width, max_q, width * cfg.page_size if max_seq is None else max_seq,
+        att = ctypes.byref(rssm_attend_config(Bn, Hq, T, width, _int("max_q", max_q),
+                                              _int("max_seq", width * cfg.page_size if max_seq is None else max_seq),
                                               D ** -0.5 if sm_scale is None else sm_scale))
         _, ws, nb = _workspace(workspace, lib.rssm_kv4_attend_workspace_bytes(kv, att), dev, q.device)
         return lib.rssm_kv4_attend(

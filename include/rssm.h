@@ -287,7 +287,9 @@ RSSM_API rssm_status rssm_mamba2_prefill(const rssm_prefill_config *cfg, const f
  *   workspace: device, 256-byte aligned, rssm_gdn_prefill_workspace_bytes(cfg) bytes (NULL
  *          where that is 0).
  * A request whose offsets are out of order or out of range sets RSSM_DEV_BAD_LENGTHS and is
- * skipped (its rows of y and S_out are left as they were). */
+ * skipped (its rows of y and S_out are left as they were); requests that overlap one another
+ * because of it hold unspecified values.  {RSSM_DEV_PIPE_TIMEOUT, b, h, token} is set if a
+ * tensor-core wait gives up (2 s). */
 typedef struct {
     int32_t batch, nheads, headdim, dstate;
     int32_t input_dtype; /* F32 | BF16 */
@@ -361,13 +363,15 @@ RSSM_API rssm_status rssm_kv4_export(const rssm_kv4_config *cfg, int32_t tokens,
  *   batch 1..65535, n_q_heads a multiple of n_kv_heads, tokens = rows of q and out,
  *   max_pages = row length of block_table (int32 [B][max_pages]), max_q >= every n,
  *   max_seq >= every seq_len (both size the launch, so that it can be captured once for
- *   growing requests; the lesser of max_seq and max_pages * page_size is at most 2^30).  q, out: device bf16 [tokens][n_q_heads][head_dim]; rows of no request
- *   are left as they were.
+ *   growing requests; the lesser of max_seq and max_pages * page_size is at most 2^30).
+ *   q, out: device bf16 [tokens][n_q_heads][head_dim]; rows of no request are left as they
+ *   were.
  *   workspace: device, 256-byte aligned, rssm_kv4_attend_workspace_bytes bytes (NULL where 0).
  * A request whose offsets or length do not fit (cu_q out of order or past tokens, n > max_q,
  * seq_len < 0, > max_seq or > max_pages * page_size) sets RSSM_DEV_BAD_LENGTHS and its rows
  * are left as they were; a page outside the cache sets RSSM_DEV_BAD_PAGE and its tokens are
- * left out as if masked. */
+ * left out as if masked; {RSSM_DEV_PIPE_TIMEOUT, b, kv head, row} is set if a tensor-core wait
+ * gives up (2 s). */
 typedef struct {
     int32_t batch, n_q_heads, tokens, max_pages, max_q, max_seq;
     float sm_scale;

@@ -576,3 +576,20 @@ def test_attend_offsets_past_32_bits():
     c = dict(q=_t(r.normal(size=(1, 16, D)), "bfloat16"), cache=cache, table=_i(table), lens=_i([L]), cu=[0, 1],
              K=[_np(hk)], V=[_np(hv)], kw={}, max_q=1)
     _attend_check(c, _attend_run(c))
+
+
+def test_sizes_that_would_wrap_are_refused():
+    import torch
+
+    one, table = _i([1]), torch.zeros((1, 2), dtype=torch.int32, device="cuda")
+    for kw in (dict(page_size=2 ** 32 + 16), dict(max_tokens=2 ** 32 + 1), dict(max_tokens=0), dict(page_size=-16)):
+        with pytest.raises(ValueError):
+            rssm.build_tables(one, one, _i([0, 1]), _i([0]), table, **{**dict(page_size=16, max_tokens=1), **kw})
+    assert not table.any()
+    cache = rssm.kv4_cache(2, 1, 16, 64)
+    q = torch.zeros((1, 2, 64), dtype=torch.bfloat16, device="cuda")
+    for kw in (dict(max_q=2 ** 32 + 1), dict(max_q=1, max_seq=2 ** 32 + 1)):
+        with pytest.raises(ValueError):
+            rssm.kv4_attend(q, cache, table, one, _i([0, 1]), **kw)
+    with pytest.raises(ValueError):
+        rssm.kv4_attend(q[:, :, :0].contiguous(), cache, table, one, _i([0, 1]), 1)
