@@ -308,14 +308,14 @@ def _opt(name, t, dtype, shape, idx):
     return None if t is None else _want(name, t, dtype, shape, idx)
 
 
-def _workspace(t, need, idx, device):
+def _workspace(t, need, idx, like):
     """(tensor, pointer, bytes) of the caller's workspace or of a new one."""
     import torch
 
     if t is None:
         if not need:
             return None, None, 0
-        t = torch.empty(need, dtype=torch.uint8, device=device)
+        t = like.new_empty(need, dtype=torch.uint8)
     return t, _want("workspace", t, torch.uint8, (t.numel(),), idx), t.numel()
 
 
@@ -358,11 +358,11 @@ def gdn_prefill(q, k, v, alpha, beta, cu_seqlens, S0=None, y=None, S_out=None, w
 
     def call(st):
         nonlocal y, S_out
-        y = torch.empty((T, H, P), dtype=f32, device=q.device) if y is None else y
-        S_out = torch.empty((Bn, H, P, N), dtype=f32, device=q.device) if S_out is None else S_out
+        y = q.new_empty((T, H, P), dtype=f32) if y is None else y
+        S_out = q.new_empty((Bn, H, P, N), dtype=f32) if S_out is None else S_out
         lib = load()
         cfg = ctypes.byref(rssm_gdn_prefill_config(Bn, H, P, N, RSSM_BF16 if dt is torch.bfloat16 else RSSM_F32, T))
-        _, ws, nb = _workspace(workspace, lib.rssm_gdn_prefill_workspace_bytes(cfg), dev, q.device)
+        _, ws, nb = _workspace(workspace, lib.rssm_gdn_prefill_workspace_bytes(cfg), dev, q)
         ins = rssm_inputs(q=_want("q", q, dt, (T, H, N), dev), k=_want("k", k, dt, (T, H, N), dev),
                           v=_want("v", v, dt, (T, H, P), dev), alpha=_want("alpha", alpha, f32, (T, H), dev),
                           beta=_want("beta", beta, f32, (T, H), dev))
@@ -392,7 +392,7 @@ def build_tables(cached_len, new_len, free_pages, free_head, block_table, page_s
 
     def call(st):
         nonlocal out
-        out = torch.empty(2 * Bn + 2 * max_tokens + 2, dtype=i32, device=cached_len.device).split_with_sizes(sizes)  # one allocation
+        out = cached_len.new_empty(2 * Bn + 2 * max_tokens + 2, dtype=i32).split_with_sizes(sizes)  # one allocation
         base = out[0].data_ptr()
         cfg = rssm_tables_config(Bn, _int("page_size", page_size), width, _int("free_pages", free_pages.shape[0]), max_tokens)
         return load().rssm_build_tables(
@@ -416,18 +416,19 @@ def kv4_cache(num_pages, n_kv_heads, page_size, head_dim, device="cuda"):
     return torch.zeros((num_pages, n_kv_heads, page_size * head_dim * 9 // 8), dtype=torch.uint8, device=device)
 
 
-def _kv4_config(cache, head_dim, k_scale, v_scale):
+def _kv4_config(cache, head_dim, k_scale, v_scale, idx):
+    """(config, pointer) of a cache on the given device."""
     import torch
 
-    if cache.dtype != torch.uint8 or cache.dim() != 3 or not cache.is_cuda or not cache.is_contiguous():
-        raise ValueError("cache: expected a contiguous CUDA uint8 tensor [pages, kv heads, page bytes]")
+    if cache.dtype is not torch.uint8 or cache.dim() != 3 or cache.get_device() != idx or not cache.is_contiguous():
+        raise ValueError(f"cache: expected a contiguous uint8 tensor [pages, kv heads, page bytes] on cuda:{idx}")
     pages, heads, nb = cache.shape
     if head_dim < 1:
         raise ValueError(f"head_dim: expected 64 or 128, got {head_dim}")
     ps = nb * 8 // (9 * head_dim)
     if ps * 9 * head_dim != nb * 8:
         raise ValueError(f"cache: {nb} bytes a page and head are no whole number of tokens of {head_dim} channels")
-    return rssm_kv4_config(heads, head_dim, ps, pages, k_scale, v_scale)
+    return rssm_kv4_config(heads, head_dim, ps, pages, k_scale, v_scale), cache.data_ptr()
 
 
 def kv4_append(k, v, slot_map, cache, k_scale=1.0, v_scale=1.0, err=None, stream=None):
@@ -438,13 +439,13 @@ def kv4_append(k, v, slot_map, cache, k_scale=1.0, v_scale=1.0, err=None, stream
     if k.dim() != 3 or cache.dim() != 3:
         raise ValueError("expected k of shape [tokens, kv heads, head_dim] and cache of [pages, kv heads, bytes]")
     dev, (T, _, D), bf = _cuda_index(k, "k"), k.shape, torch.bfloat16
-    cfg = _kv4_config(cache, D, k_scale, v_scale)
+    cfg, held = _kv4_config(cache, D, k_scale, v_scale, dev)
     sh = (T, cache.shape[1], D)
 
     def call(st):
         return load().rssm_kv4_append(
             ctypes.byref(cfg), T, _want("k", k, bf, sh, dev), _want("v", v, bf, sh, dev),
-            _want("slot_map", slot_map, torch.int32, (T,), dev), _want("cache", cache, torch.uint8, cache.shape, dev),
+            _want("slot_map", slot_map, torch.int32, (T,), dev), held,
             _opt("err", err, torch.int32, (4,), dev), st)
 
     _ok(_run(call, dev, stream, (k, v, slot_map, cache, err)), "rssm_kv4_append")
@@ -458,17 +459,17 @@ def kv4_export(slot_map, cache, head_dim, k_scale=1.0, v_scale=1.0, k=None, v=No
     dev, bf = _cuda_index(slot_map, "slot_map"), torch.bfloat16
     if cache.dim() != 3 or slot_map.dim() != 1:
         raise ValueError("expected slot_map of shape [tokens] and cache of [pages, kv heads, bytes]")
-    cfg = _kv4_config(cache, head_dim, k_scale, v_scale)
+    cfg, held = _kv4_config(cache, head_dim, k_scale, v_scale, dev)
     T = slot_map.shape[0]
     sh = (T, cache.shape[1], head_dim)
 
     def call(st):
         nonlocal k, v
-        k = torch.empty(sh, dtype=bf, device=cache.device) if k is None else k
-        v = torch.empty(sh, dtype=bf, device=cache.device) if v is None else v
+        k = cache.new_empty(sh, dtype=bf) if k is None else k
+        v = cache.new_empty(sh, dtype=bf) if v is None else v
         return load().rssm_kv4_export(
             ctypes.byref(cfg), T, _want("slot_map", slot_map, torch.int32, (T,), dev),
-            _want("cache", cache, torch.uint8, cache.shape, dev), _want("k", k, bf, sh, dev),
+            held, _want("k", k, bf, sh, dev),
             _want("v", v, bf, sh, dev), _opt("err", err, torch.int32, (4,), dev), st)
 
     _ok(_run(call, dev, stream, (slot_map, cache, k, v, err)), "rssm_kv4_export")
@@ -489,19 +490,19 @@ def kv4_attend(q, cache, block_table, seq_len, cu_q, max_q, k_scale=1.0, v_scale
         raise ValueError("expected q [tokens, heads, head_dim], cache [pages, kv heads, bytes], block_table "
                          "[requests, pages] and seq_len [requests]")
     dev, (T, Hq, D), bf, i32 = _cuda_index(q, "q"), q.shape, torch.bfloat16, torch.int32
-    cfg = _kv4_config(cache, D, k_scale, v_scale)
+    cfg, held = _kv4_config(cache, D, k_scale, v_scale, dev)
     Bn, width = block_table.shape
 
     def call(st):
         nonlocal out
-        out = torch.empty((T, Hq, D), dtype=bf, device=q.device) if out is None else out
+        out = q.new_empty((T, Hq, D), dtype=bf) if out is None else out
         lib, kv = load(), ctypes.byref(cfg)
         att = ctypes.byref(rssm_attend_config(Bn, Hq, T, width, _int("max_q", max_q),
                                               _int("max_seq", width * cfg.page_size if max_seq is None else max_seq),
                                               D ** -0.5 if sm_scale is None else sm_scale))
-        _, ws, nb = _workspace(workspace, lib.rssm_kv4_attend_workspace_bytes(kv, att), dev, q.device)
+        _, ws, nb = _workspace(workspace, lib.rssm_kv4_attend_workspace_bytes(kv, att), dev, q)
         return lib.rssm_kv4_attend(
-            kv, att, _want("q", q, bf, (T, Hq, D), dev), _want("cache", cache, torch.uint8, cache.shape, dev),
+            kv, att, _want("q", q, bf, (T, Hq, D), dev), held,
             _want("block_table", block_table, i32, (Bn, width), dev), _want("seq_len", seq_len, i32, (Bn,), dev),
             _want("cu_q", cu_q, i32, (Bn + 1,), dev), _want("out", out, bf, (T, Hq, D), dev), ws, nb,
             _opt("err", err, i32, (4,), dev), st)
