@@ -199,6 +199,8 @@ class HybridStack:
         if self.pos >= self.cap:
             raise RuntimeError("the attention cache is full; build the stack with a larger max_steps")
         if self.kv_cache == "fp4":
+            if self.torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("a step of the stack advances counters on the host, which a replayed graph would not")
             self._tables(self.one_new, self.s.batch)
         for kind, p in self.layers:
             x = self._ssm(x, p) if kind == "ssm" else self._attn(x, p)

@@ -205,3 +205,18 @@ def test_hybrid_stack_with_a_4bit_cache(context, page):
     with pytest.raises(ValueError, match="kv_cache"):
         HybridStack(shape, kv_cache="fp8")
     assert torch.equal(plain.layers[1][1]["wq"], st.layers[1][1]["wq"])
+
+
+def test_hybrid_stack_with_a_4bit_cache_refuses_capture(monkeypatch):
+    import torch
+
+    st = HybridStack(SHAPE, seed=7, max_steps=4, kv_cache="fp4")
+    x = torch.zeros((SHAPE.batch, SHAPE.d_model), dtype=torch.bfloat16, device="cuda")
+    before = st.cached_len.tolist()
+    with monkeypatch.context() as m:
+        m.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+        with pytest.raises(RuntimeError, match="replayed graph"):
+            st.step(x)
+    assert st.cached_len.tolist() == before and st.pos == SHAPE.context
+    st.step(x)
+    assert st.cached_len.tolist() == [n + 1 for n in before]
