@@ -28,7 +28,7 @@
 //
 // 64 prompts of 1 to 1024 tokens (34500 in all), 32 heads, P = 128: 394 us for the chunk kernel and 472 for the
 // scan, of 259 at the rate of a copy for both (together 2.0 TB/s of what a call has to move).  The chunk kernel is
-// bound by the issue of its fp32 work in shared memory (1.7 instructions a cycle at four CTAs an SM, which its
+// bound by the issue of its fp32 work in shared memory (2.0 instructions a cycle at four CTAs an SM, which its
 // shared memory and registers allow).  The scan is a chain: 2.6 us a chunk of a prompt, three products that wait
 // for each other and the conversions between them, with one CTA an SM, and about 13 us to start and end a CTA.  One
 // prompt of 8191 tokens: 94 and 330 us.

@@ -32,7 +32,7 @@
 // matrix instruction takes 8 slots and the widening of its operands about as many: a 16-row tile uses half of
 // the columns that a 16 x 8 product offers, so that more rows a tile are nearly free (32 rows: two products for one
 // widening).  Widening to shared memory first, wider copies and fewer warps with more stages were slower; a third
-// CTA on the SM (80 registers a thread) is worth more than any of them.
+// CTA on the SM (160 registers a thread) is worth more than any of them.
 #include <math.h>
 
 #include "rssm_internal.h"
