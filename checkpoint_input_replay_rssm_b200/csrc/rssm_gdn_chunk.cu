@@ -471,16 +471,9 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const GdnPreA
     const int nchunks = (r1 - r0 + kC - 1) / kC;
     const int64_t v_row = (int64_t)H * P;
 
-    // Wait for a barrier's phase; false, for every role, once any wait has run out.
+    // Wait for a barrier's phase, a warp at a time; false, for every role, once any wait has run out.
     auto wait_for = [&](int which, int parity) {
-        if (!bar_try(bar + which, parity)) {
-            const long long t0 = clock64();
-            while (!bar_try(bar + which, parity))
-                if (*sfail || clock64() - t0 > kWaitCycles) {
-                    *sfail = 1;
-                    return false;
-                }
-        }
+        if (!warp_wait(bar + which, parity, sfail)) return false;
         tc_fence_after();
         return true;
     };
@@ -678,7 +671,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const GdnPreA
             arrive(kBarIn + (c & 1));
         }
         cp_async_wait_all();
-        if (*sfail && warp == kFirstIn)  // copies that may still be in flight
+        if (warp == kFirstIn && warp_failed(sfail))  // copies that may still be in flight
             for (int i = 0; i < 4; ++i) bar_wait(bar + kBarOp + (i & 1), i >> 1);
     } else {
         const bool lead = elect_one();
@@ -733,7 +726,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const GdnPreA
             if (c + 1 < nchunks && !wait_for(kBarIn + (par ^ 1), ((c + 1) >> 1) & 1)) break;
             if (lead) umma_commit(bar + kBarZq);
         }
-        if (*sfail) {  // products that may still run
+        if (warp_failed(sfail)) {  // products that may still run
             if (lead) umma_commit(bar + kBarDrain);
             __syncwarp();
             bar_wait(bar + kBarDrain, 0);

@@ -92,16 +92,9 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tslot, base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-    // Wait for a barrier's phase; false, for every role, once any wait has run out.
+    // Wait for a barrier's phase, a warp at a time; false, for every role, once any wait has run out.
     auto wait_for = [&](int which, int parity) {
-        if (!bar_try(bar + which, parity)) {
-            const long long t0 = clock64();
-            while (!bar_try(bar + which, parity))
-                if (*sfail || clock64() - t0 > kWaitCycles) {
-                    *sfail = 1;
-                    return false;
-                }
-        }
+        if (!warp_wait(bar + which, parity, sfail)) return false;
         tc_fence_after();
         return true;
     };
@@ -325,7 +318,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
                 }
             }
         }
-        if (*sfail && issues) {  // products that may still run
+        if (issues && warp_failed(sfail)) {  // products that may still run
             if (lead) umma_commit(bar + kBarDrain + st);
             __syncwarp();
             bar_wait(bar + kBarDrain + st, 0);

@@ -15,6 +15,7 @@
 #include <stdint.h>
 
 #include "rssm_pipe.cuh"
+#include "rssm_wait.h"
 
 namespace rssm {
 
@@ -250,6 +251,23 @@ __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity) {
         if (clock64() - t0 > kWaitCycles) return false;
     return true;
 }
+// The same by a whole warp in a CTA whose roles wait for each other: one outcome for all its lanes, and false, for every
+// role, once any wait has run out (*fail).
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *fail) {
+    long long t0 = 0;
+    const bool ok = wait_together([&] { return bar_try(bar, parity); },
+                                  [&] {
+                                      const long long t = clock64();
+                                      if (t0 == 0) t0 = t;
+                                      return *fail != 0 || t - t0 > kWaitCycles;
+                                  },
+                                  [](bool x) { return __all_sync(0xffffffffu, x) != 0; },
+                                  [](bool x) { return __any_sync(0xffffffffu, x) != 0; });
+    if (!ok) *fail = 1;
+    return ok;
+}
+// Whether some wait has failed, as one lane sees it: the same for the warp.
+__device__ __forceinline__ bool warp_failed(volatile int *fail) { return __any_sync(0xffffffffu, *fail != 0); }
 
 __device__ __forceinline__ float ex2(float x) {
     float r;
