@@ -186,7 +186,8 @@ extern "C" RSSM_API rssm_status rssm_build_tables(const rssm_tables_config *cfg,
     TablesArgs a{c.batch, c.page_size, c.max_pages, c.num_free, c.max_tokens, cached_len, new_len, free_pages,
                  free_head, block_table, cu_new, seq_len, slot_map, position, next_free, dev_error};
     const size_t smem = (size_t)(2 * (c.batch + 1)) * sizeof(int);
-    if (smem > 48 * 1024 && cudaFuncSetAttribute(tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    // What needs no permission is 48 KiB of the sums and the kernel's own arrays together (less than 1 KiB of them).
+    if (smem > 47 * 1024 && cudaFuncSetAttribute(tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                  2 * (kMaxRequests + 1) * (int)sizeof(int)) != cudaSuccess)
         return RSSM_ECUDA;
     const int64_t work = c.max_tokens > c.batch ? c.max_tokens : c.batch;
