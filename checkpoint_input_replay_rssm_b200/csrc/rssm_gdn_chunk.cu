@@ -23,8 +23,9 @@
 // bits and kept as two fp32, so that a difference between neighbours is exact to fp32 however far
 // down the chunk they are.
 //
-// Request b's chunk c has slot r0 / 64 + b + c (r0 its first row): slots do not collide, since
-// floor((x + len) / 64) + 1 >= ceil(len / 64), and no prefix sum over the requests is needed.
+// Request b's chunk c has slot first[b] + c, first[] a prefix sum that a CTA launched before makes (rssm_gdn_plan.cuh).
+// It takes nothing from the offsets on trust; slots at r0 / 64 + b + c, which need no sum, are distinct only where
+// every request's offsets are in order.
 //
 // 64 prompts of 1 to 1024 tokens (34500 in all), 32 heads, P = 128: 394 us for the chunk kernel and 472 for the
 // scan, of 259 at the rate of a copy for both (together 2.0 TB/s of what a call has to move).  The chunk kernel is
@@ -34,15 +35,14 @@
 // prompt of 8191 tokens: 94 and 330 us.
 #include <cuda_bf16.h>
 
-#include "rssm_gdn_prefill.h"
-#include "rssm_packed.cuh"
+#include "rssm_gdn_plan.cuh"
 #include "rssm_umma.cuh"
 
 namespace rssm {
 
 namespace {
 
-constexpr int kC = 64;                  // chunk
+constexpr int kC = kGdnChunk;           // 64 tokens
 constexpr int kDk = 128;                // state columns (N)
 constexpr int kTile = 128 * kC * 2;     // [128 x 64] bf16
 constexpr int kSlot = 2 * kTile + 512;  // hi, lo, then 2^Lam_i and 2^{Lam_C - Lam_i} fp32
@@ -66,6 +66,12 @@ __device__ __forceinline__ void split8(const float *v, uint4 &hi, uint4 &lo) {
 __device__ __forceinline__ void bulk_s2g(void *dst, const void *src, uint32_t bytes) {
     asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
                  : "memory");
+}
+
+constexpr int kPlanThreads = 128;
+__global__ void __launch_bounds__(kPlanThreads) gdn_plan_kernel(const GdnPreArgs a) {
+    pdl_trigger();
+    gdn_plan<kPlanThreads>(a);
 }
 
 // ---------------------------------------------------------------- chunk operands
@@ -94,17 +100,21 @@ __global__ void __launch_bounds__(kChunkThreads, 4) gdn_chunk_kernel(const GdnPr
     int *sfound = reinterpret_cast<int *>(bar + 2);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int slot = blockIdx.x, h = blockIdx.y, H = a.H;
-    // The request of this slot: the last b with cu[b] / 64 + b <= slot, 32 candidates a round.
+    // The request of this slot: the last b with first[b] <= slot, 32 candidates a round.
     if (warp == 0) {
+        pdl_wait();
         int lo = 0, n = a.B;  // b is in [lo, lo + n)
         while (n > 1) {
             const int step = (n + 31) / 32, at = lo + lane * step;
-            const bool le = lane * step < n && (lane == 0 || a.cu[at] / kC + at <= slot);
+            const bool le = lane * step < n && (lane == 0 || a.first[at] <= slot);
             const int last = 31 - __clz(__ballot_sync(0xffffffffu, le));
             n = min(step, n - last * step);
             lo += last * step;
         }
-        if (lane == 0) *sfound = lo;
+        if (lane == 0) {
+            sfound[0] = lo;
+            sfound[1] = slot - a.first[lo];
+        }
     } else if (warp == 1) {
         tmem_alloc(tslot, 128);
         if (lane == 0) {
@@ -119,11 +129,10 @@ __global__ void __launch_bounds__(kChunkThreads, 4) gdn_chunk_kernel(const GdnPr
     // memory: one of them has all of an SM's.
     pdl_trigger();
     const uint32_t tmem = *tslot;
-    const int b = *sfound;
+    const int b = sfound[0], c = sfound[1];
     int r0, r1;
-    const bool ok = packed_rows(a.cu, b, a.tokens, r0, r1);
-    const int c = slot - (r0 / kC + b), t0 = r0 + c * kC;
-    const bool work = ok && c >= 0 && t0 < r1;
+    const bool work = c < gdn_chunks(a, b, r0, r1);
+    const int t0 = work ? r0 + c * kC : 0;
     bool failed = false;
     if (work) {
         const int Lc = min(kC, r1 - t0);
@@ -425,6 +434,7 @@ struct ScanSmem {
 constexpr int kChainWarps = 16, kOutWarps = 4, kInWarps = 3;
 constexpr int kFirstIn = kChainWarps + kOutWarps, kIssuer = kFirstIn + kInWarps;
 constexpr int kScanThreads = 32 * (kIssuer + 1);
+constexpr int kNoSlots = 2;  // (a failure of its own kind) more chunks than rows have: requests that overlap
 enum ScanBar {
     kBarYk, kBarZk, kBarS, kBarZq,  // products done (one phase a chunk)
     kBarPutS, kBarPutR, kBarPutU,   // operands in place (every chain warp arrives)
@@ -656,23 +666,31 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const GdnPreA
                 src += step;
             }
         };
-        if (warp == kFirstIn) pdl_wait();  // the chunk kernel's operands are there
+        int64_t slot0 = 0;
+        if (warp == kFirstIn) {
+            pdl_wait();  // the chunk kernel's operands are there
+            slot0 = a.first[b];
+            if (slot0 + nchunks > a.slots) *sfail = kNoSlots;
+        }
+        int copies = 0;
         for (int c = 0; c < nchunks; ++c) {
+            if (warp == kFirstIn && warp_failed(sfail)) break;
             if (c >= 2 && !wait_for(kBarZq, c & 1)) break;  // chunk c - 2's products are done
             load(c);
             if (c >= 2 && !wait_for(kBarO, c & 1)) break;   // and its decays read
             if (warp == kFirstIn && lane == 0) {
                 uint64_t *br = bar + kBarOp + (c & 1);
                 mbar_arrive_expect_tx(br, kSlot);
-                bulk_g2s(sm + L::kOp + (c & 1) * L::kOpStep, a.ws + ((int64_t)(r0 / kC + b + c) * H + h) * kSlot, kSlot, br);
+                bulk_g2s(sm + L::kOp + (c & 1) * L::kOpStep, a.ws + ((slot0 + c) * H + h) * kSlot, kSlot, br);
             }
+            copies = c + 1;
             cp_async_wait_all();
             fence_async_smem();
             arrive(kBarIn + (c & 1));
         }
         cp_async_wait_all();
         if (warp == kFirstIn && warp_failed(sfail))  // copies that may still be in flight
-            for (int i = 0; i < 4; ++i) bar_wait(bar + kBarOp + (i & 1), i >> 1);
+            for (int c = max(0, copies - 2); c < copies; ++c) bar_wait(bar + kBarOp + (c & 1), (c >> 1) & 1);
     } else {
         const bool lead = elect_one();
         for (int c = 0; c < nchunks; ++c) {
@@ -734,34 +752,46 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const GdnPreA
     }
     tc_fence_before();
     __syncthreads();
-    if (*sfail && tid == 0) report_opt(a.err, DEV_PIPE_TIMEOUT, b, h, 0);
+    if (*sfail && tid == 0) report_opt(a.err, *sfail == kNoSlots ? DEV_BAD_LENGTHS : DEV_PIPE_TIMEOUT, b, h, 0);
     if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
-int64_t slots(int B, int tokens) { return (int64_t)tokens / kC + B + 1; }
+// Chunks of requests that do not overlap: at most one more than their share of the rows each.
+int64_t slots_of(int B, int tokens) { return (int64_t)tokens / kC + B; }
+size_t plan_bytes(int B) { return ((size_t)B * sizeof(int32_t) + 255) / 256 * 256; }
 
-}  // namespace
-
-size_t gdn_chunk_bytes(int B, int H, int tokens) { return (size_t)(slots(B, tokens) * H) * kSlot; }
-
-cudaError_t gdn_chunk_launch(const GdnPreArgs &a, cudaStream_t st) {
-    const int s1 = ChunkSmem::kBytes + 1024, s2 = ScanSmem::kBytes + 1024;
-    cudaError_t e = cudaFuncSetAttribute(gdn_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, s1);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(gdn_scan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, s2);
-    if (e != cudaSuccess) return e;
-    gdn_chunk_kernel<<<dim3((unsigned)slots(a.B, a.tokens), a.H), kChunkThreads, s1, st>>>(a);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+cudaError_t launch_after(const void *kernel, dim3 grid, int threads, size_t smem, GdnPreArgs a, cudaStream_t st) {
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(a.H * ((a.P + 127) / 128), a.B);
-    cfg.blockDim = dim3(kScanThreads);
-    cfg.dynamicSmemBytes = s2;
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, gdn_scan_kernel, a);
+    void *args[] = {&a};
+    return cudaLaunchKernelExC(&cfg, kernel, args);
+}
+
+}  // namespace
+
+size_t gdn_chunk_bytes(int B, int H, int tokens) { return plan_bytes(B) + (size_t)(slots_of(B, tokens) * H) * kSlot; }
+
+cudaError_t gdn_chunk_launch(GdnPreArgs a, uint8_t *workspace, cudaStream_t st) {
+    const int s1 = ChunkSmem::kBytes + 1024, s2 = ScanSmem::kBytes + 1024;
+    cudaError_t e = cudaFuncSetAttribute(gdn_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, s1);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(gdn_scan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, s2);
+    if (e != cudaSuccess) return e;
+    a.slots = (int)slots_of(a.B, a.tokens);
+    a.first = reinterpret_cast<int32_t *>(workspace);
+    a.ws = workspace + plan_bytes(a.B);
+    gdn_plan_kernel<<<1, kPlanThreads, 0, st>>>(a);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    e = launch_after((const void *)gdn_chunk_kernel, dim3(a.slots, a.H), kChunkThreads, s1, a, st);
+    if (e != cudaSuccess) return e;
+    return launch_after((const void *)gdn_scan_kernel, dim3(a.H * ((a.P + 127) / 128), a.B), kScanThreads, s2, a, st);
 }
 
 }  // namespace rssm

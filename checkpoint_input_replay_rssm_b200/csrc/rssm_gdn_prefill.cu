@@ -244,8 +244,8 @@ RSSM_API rssm_status rssm_gdn_prefill(const rssm_gdn_prefill_config *cfg, const 
     if (need && (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 255))) return RSSM_EINVAL;
     const rssm_gdn_prefill_config &c = *cfg;
     const GdnPreArgs a{c.batch, c.nheads, c.headdim, c.tokens, in->q, in->k, in->v, in->alpha, in->beta,
-                       cu, S0, y, S_out, (uint8_t *)workspace, dev_error};
-    const cudaError_t e = gdn_chunked(c) ? gdn_chunk_launch(a, (cudaStream_t)stream)
+                       cu, S0, y, S_out, 0, nullptr, nullptr, dev_error};
+    const cudaError_t e = gdn_chunked(c) ? gdn_chunk_launch(a, (uint8_t *)workspace, (cudaStream_t)stream)
                           : c.input_dtype == RSSM_BF16 ? launch_recurrent<__nv_bfloat16>(a, c.dstate, (cudaStream_t)stream)
                                                      : launch_recurrent<float>(a, c.dstate, (cudaStream_t)stream);
     return e == cudaSuccess ? RSSM_OK : RSSM_ECUDA;

@@ -14,12 +14,15 @@ struct GdnPreArgs {
     const int32_t *cu;          // [B + 1]
     const float *S0;            // [B][H][P][N] or nullptr
     float *y, *S_out;
-    uint8_t *ws;  // chunk operands (chunked form)
+    // chunked form, in the workspace
+    int slots;       // chunks that there is room for
+    int32_t *first;  // [B] slot of each request's first chunk
+    uint8_t *ws;     // [slots][H] chunk operands
     int32_t *err;
 };
 
-// Chunked form on the tensor cores: N = 128, bf16 inputs, P a multiple of 64.
+// Chunked form on the tensor cores: N = 128, bf16 inputs, P a multiple of 8.  Its part of the workspace, and the call.
 size_t gdn_chunk_bytes(int B, int H, int tokens);
-cudaError_t gdn_chunk_launch(const GdnPreArgs &a, cudaStream_t st);
+cudaError_t gdn_chunk_launch(GdnPreArgs a, uint8_t *workspace, cudaStream_t st);
 
 }  // namespace rssm

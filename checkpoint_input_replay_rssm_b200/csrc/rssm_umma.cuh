@@ -263,7 +263,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
                                   },
                                   [](bool x) { return __all_sync(0xffffffffu, x) != 0; },
                                   [](bool x) { return __any_sync(0xffffffffu, x) != 0; });
-    if (!ok) *fail = 1;
+    if (!ok && !*fail) *fail = 1;
     return ok;
 }
 // Whether some wait has failed, as one lane sees it: the same for the warp.

@@ -287,9 +287,10 @@ RSSM_API rssm_status rssm_mamba2_prefill(const rssm_prefill_config *cfg, const f
  *   workspace: device, 256-byte aligned, rssm_gdn_prefill_workspace_bytes(cfg) bytes (NULL
  *          where that is 0).
  * A request whose offsets are out of order or out of range sets RSSM_DEV_BAD_LENGTHS and is
- * skipped (its rows of y and S_out are left as they were); requests that overlap one another
- * because of it hold unspecified values.  {RSSM_DEV_PIPE_TIMEOUT, b, h, token} is set if a
- * tensor-core wait gives up (2 s). */
+ * skipped (its rows of y and S_out are left as they were).  Every other request is served as if
+ * it were alone, but for those that share rows with one another: they hold unspecified values, or
+ * are skipped with the same code where together they claim more rows than there are.
+ * {RSSM_DEV_PIPE_TIMEOUT, b, h, token} is set if a tensor-core wait gives up (2 s). */
 typedef struct {
     int32_t batch, nheads, headdim, dstate;
     int32_t input_dtype; /* F32 | BF16 */

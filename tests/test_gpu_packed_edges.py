@@ -10,7 +10,7 @@ import pytest
 
 from checkpoint_input_replay_rssm_b200 import rssm
 from oracle import packed
-from tests.test_gpu_packed import _i, _tables_case, _tables_run
+from tests.test_gpu_packed import _close, _cu, _err, _gdn_inputs, _gdn_ref, _gdn_run, _i, _np, _t, _tables_case, _tables_run
 
 pytestmark = pytest.mark.gpu
 
@@ -33,3 +33,77 @@ def test_tables_of_batches_around_the_shared_memory_that_needs_no_permission(B):
     code = f"from tests.test_gpu_packed_edges import _tables_equal; _tables_equal({B})"
     done = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert done.returncode == 0, done.stderr[-2000:]
+
+
+# ---------------------------------------------------------------- gated delta rule
+def _offsets(what):
+    """Offsets of requests some of which are bad, and their number of rows."""
+    if what == "too large among many":
+        cu = list(range(0, 6500, 100))
+        cu[2] = 10 ** 6
+        return cu, 6400
+    if what == "negative in the middle":
+        return [0, 100, -100000, 300, 400], 400
+    if what == "descending to rows of their own":
+        return [100, 200, 0, 100, 50, 50], 200  # requests 0 and 2 are whole and share no row, 1 and 3 are bad
+    cu = list(range(0, 26 * 41, 26))
+    for b in range(3, 41, 7):
+        cu[b] = (-5, 2 ** 31 - 1, -2 ** 31, 10 ** 5, 2000, -1)[b % 6]
+    return cu, 26 * 40
+
+
+@pytest.mark.parametrize("what", ["too large among many", "negative in the middle", "descending to rows of their own",
+                                  "several among many"])
+def test_gdn_a_bad_offset_spoils_no_other_request(what):
+    import torch
+
+    cu, T = _offsets(what)
+    B, H, P = len(cu) - 1, 2, 64
+    d, _, _ = _gdn_inputs([T], H, 128, P, "bfloat16", 31, state=False)
+    S0 = _t(0.1 * np.random.default_rng(32).normal(size=(B, H, P, 128)))
+    good = [b for b in range(B) if 0 <= cu[b] <= cu[b + 1] <= T]
+    assert 0 < len(good) < B
+    err, y, So = _err(), torch.full((T, H, P), 7.25, device="cuda"), torch.full_like(S0, 7.25)
+    ws = torch.full((1 << 26,), 0xFF, dtype=torch.uint8, device="cuda")  # NaN where operands are missing
+    rssm.gdn_prefill(d["q"], d["k"], d["v"], d["alpha"], d["beta"], _i(cu), S0, y=y, S_out=So, err=err, workspace=ws)
+    assert err[0].item() == rssm.RSSM_DEV_BAD_LENGTHS and err[1].item() not in good
+    owned = np.zeros(T, bool)
+    for b in range(B):
+        if b not in good:
+            assert (So[b] == 7.25).all(), b
+            continue
+        rows = slice(cu[b], cu[b + 1])
+        want, Sw = packed.gdn(*(_np(d[n])[rows] for n in ("q", "k", "v", "alpha", "beta")), [0, cu[b + 1] - cu[b]], _np(S0)[b:b + 1])
+        _close(_np(y)[rows], want, b)
+        _close(_np(So)[b:b + 1], Sw, b)
+        owned[rows] = True
+    assert (y[_t(~owned, "bool")] == 7.25).all(), "rows of no request were written"
+
+
+def test_gdn_requests_that_overlap_past_all_room_are_reported():
+    """Six requests that each claim all rows (every second offset goes back to 0) ask for more chunks than these rows
+    can have; the call ends at once and says so."""
+    import time
+
+    import torch
+
+    cu = [0, 600] * 6
+    d, _, _ = _gdn_inputs([600], 2, 128, 64, "bfloat16", 33, state=False)
+    err = _err()
+    torch.cuda.synchronize()
+    t0 = time.monotonic()
+    rssm.gdn_prefill(d["q"], d["k"], d["v"], d["alpha"], d["beta"], _i(cu), err=err)
+    assert err[0].item() == rssm.RSSM_DEV_BAD_LENGTHS and time.monotonic() - t0 < 1.0
+    y, S = _gdn_run(d, [0, 600], None)
+    want, Sw = _gdn_ref(d, [0, 600], None)
+    _close(y, want, "the next call")
+    _close(S, Sw, "the next call")
+
+
+def test_gdn_more_requests_than_one_round_of_the_search():
+    lens = [(7 * b) % 90 for b in range(70)] + [200, 0, 0, 65]
+    d, cu, S0 = _gdn_inputs(lens, 2, 128, 64, "bfloat16", 34, first=2, pad=70)
+    y, S = _gdn_run(d, cu, S0)
+    want, Sw = _gdn_ref(d, cu, S0)
+    _close(y, want, "y")
+    _close(S, Sw, "state")
