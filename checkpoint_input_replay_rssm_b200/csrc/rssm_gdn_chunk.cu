@@ -23,7 +23,7 @@
 // bits and kept as two fp32, so that a difference between neighbours is exact to fp32 however far
 // down the chunk they are.
 //
-// Request b's chunk c has slot first[b] + c, first[] a prefix sum that a CTA launched before makes (rssm_gdn_plan.cuh).
+// Request b's chunk c has slot first[b] + c, first[] a prefix sum that a kernel before makes (rssm_gdn_plan.cuh).
 // It takes nothing from the offsets on trust; slots at r0 / 64 + b + c, which need no sum, are distinct only where
 // every request's offsets are in order.
 //
@@ -68,12 +68,6 @@ __device__ __forceinline__ void bulk_s2g(void *dst, const void *src, uint32_t by
                  : "memory");
 }
 
-constexpr int kPlanThreads = 128;
-__global__ void __launch_bounds__(kPlanThreads) gdn_plan_kernel(const GdnPreArgs a) {
-    pdl_trigger();
-    gdn_plan<kPlanThreads>(a);
-}
-
 // ---------------------------------------------------------------- chunk operands
 constexpr int kLd = 68;  // fp32 row of A and T: 16-byte aligned, rows 4 banks apart
 constexpr int kChunkThreads = 256;
@@ -86,49 +80,30 @@ struct ChunkSmem {
     static constexpr int kBytes = kBar + 32;
 };
 
-// Between the two products the work is fp32 out of shared memory in short steps with barriers between them: four CTAs
-// to an SM fill each other's waits, for which T takes A's place and the operand that of K and Q.
-__global__ void __launch_bounds__(kChunkThreads, 4) gdn_chunk_kernel(const GdnPreArgs a) {
+// One chunk and head.  The barrier is in its first phase before and after; true where a wait gave up.
+__device__ __forceinline__ bool chunk_unit(const GdnPreArgs &a, uint8_t *sm, uint64_t *bar, int *sfound, uint32_t tmem, int slot, int h) {
     using L = ChunkSmem;
-    extern __shared__ __align__(1024) uint8_t raw[];
-    uint8_t *sm = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
     uint8_t *sKQ = sm + L::kKQ, *sHi = sm + L::kHi, *sLo = sm + L::kLo;
     float *sA = reinterpret_cast<float *>(sm + L::kA);
     float *lamh = reinterpret_cast<float *>(sm + L::kLam), *laml = lamh + kC, *sbeta = laml + kC, *sg = sbeta + kC;
-    uint64_t *bar = reinterpret_cast<uint64_t *>(sm + L::kBar);
-    uint32_t *tslot = reinterpret_cast<uint32_t *>(bar + 1);
-    int *sfound = reinterpret_cast<int *>(bar + 2);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int slot = blockIdx.x, h = blockIdx.y, H = a.H;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, H = a.H;
     // The request of this slot: the last b with first[b] <= slot, 32 candidates a round.
     if (warp == 0) {
-        pdl_wait();
+        const int32_t *first = gdn_first(a);
         int lo = 0, n = a.B;  // b is in [lo, lo + n)
         while (n > 1) {
             const int step = (n + 31) / 32, at = lo + lane * step;
-            const bool le = lane * step < n && (lane == 0 || a.first[at] <= slot);
+            const bool le = lane * step < n && (lane == 0 || first[at] <= slot);
             const int last = 31 - __clz(__ballot_sync(0xffffffffu, le));
             n = min(step, n - last * step);
             lo += last * step;
         }
         if (lane == 0) {
             sfound[0] = lo;
-            sfound[1] = slot - a.first[lo];
-        }
-    } else if (warp == 1) {
-        tmem_alloc(tslot, 128);
-        if (lane == 0) {
-            mbar_init(bar, 1);
-            mbar_init_fence();
+            sfound[1] = slot - first[lo];
         }
     }
-    tc_fence_before();
     __syncthreads();
-    tc_fence_after();
-    // The scan's CTAs may start (they read this kernel's results behind their own wait), once this one has its tensor
-    // memory: one of them has all of an SM's.
-    pdl_trigger();
-    const uint32_t tmem = *tslot;
     const int b = sfound[0], c = sfound[1];
     int r0, r1;
     const bool work = c < gdn_chunks(a, b, r0, r1);
@@ -400,6 +375,42 @@ __global__ void __launch_bounds__(kChunkThreads, 4) gdn_chunk_kernel(const GdnPr
         }
         if (failed && tid == 0) report_opt(a.err, DEV_PIPE_TIMEOUT, b, h, t0);
     }
+    return failed;
+}
+
+// Between the two products the work is fp32 out of shared memory in short steps with barriers between them: four CTAs
+// to an SM fill each other's waits, for which T takes A's place and the operand that of K and Q.  How many chunks there
+// are is known on the device only: the CTAs share them out.
+__global__ void __launch_bounds__(kChunkThreads, 4) gdn_chunk_kernel(const GdnPreArgs a) {
+    using L = ChunkSmem;
+    extern __shared__ __align__(1024) uint8_t raw[];
+    uint8_t *sm = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+    uint64_t *bar = reinterpret_cast<uint64_t *>(sm + L::kBar);
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(bar + 1);
+    const int warp = threadIdx.x >> 5;
+    pdl_wait();
+    const int chunks = min(a.plan[kPlanChunks], a.slots), units = chunks * a.H;
+    if ((int)blockIdx.x >= units) return;
+    if (warp == 1) {
+        tmem_alloc(tslot, 128);
+        if (elect_one()) {
+            mbar_init(bar, 1);
+            mbar_init_fence();
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    // The scan's CTAs may start (they read this kernel's results behind their own wait), once this one has its tensor
+    // memory: one of them has all of an SM's.
+    pdl_trigger();
+    const uint32_t tmem = *tslot;
+    for (int u = blockIdx.x; u < units; u += gridDim.x) {
+        if (chunk_unit(a, sm, bar, reinterpret_cast<int *>(bar + 2), tmem, u % chunks, u / chunks)) break;
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+    }
     tc_fence_before();
     __syncthreads();
     if (warp == 1) tmem_dealloc(tmem, 128);
@@ -434,7 +445,6 @@ struct ScanSmem {
 constexpr int kChainWarps = 16, kOutWarps = 4, kInWarps = 3;
 constexpr int kFirstIn = kChainWarps + kOutWarps, kIssuer = kFirstIn + kInWarps;
 constexpr int kScanThreads = 32 * (kIssuer + 1);
-constexpr int kNoSlots = 2;  // (a failure of its own kind) more chunks than rows have: requests that overlap
 enum ScanBar {
     kBarYk, kBarZk, kBarS, kBarZq,  // products done (one phase a chunk)
     kBarPutS, kBarPutR, kBarPutU,   // operands in place (every chain warp arrives)
@@ -455,13 +465,20 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const GdnPreA
     uint32_t *tslot = reinterpret_cast<uint32_t *>(bar + kBarN);
     volatile int *sfail = reinterpret_cast<volatile int *>(tslot + 1);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int slices = (a.P + 127) / 128, h = blockIdx.x / slices, p_base = (blockIdx.x % slices) * 128, b = blockIdx.y;
+    const int slices = (a.P + 127) / 128, h = blockIdx.x / slices, p_base = (blockIdx.x % slices) * 128;
     const int H = a.H, P = a.P;
     const int p_here = min(128, P - p_base);  // state rows of this CTA
-    int r0, r1;
-    if (!packed_rows(a.cu, b, a.tokens, r0, r1)) {
+    pdl_trigger();  // the recurrence's CTAs, for the short requests, take what SMs this kernel leaves
+    // The plan is complete: the chunk kernel lets this one start behind its own wait for it.  (Not through L1, which may
+    // hold what the call before had there.)
+    const int4 mine = __ldcg(gdn_order(a) + blockIdx.y);  // on its way while it is not known whether there is one
+    if ((int)blockIdx.y >= __ldcg(a.plan + kPlanRequests)) {
+        if (blockIdx.x == 0 && blockIdx.y == 0) pdl_wait();  // this kernel does not end before the chunk kernel has
+        return;
+    }
+    const int b = mine.x, slot0 = mine.y, r0 = mine.z, r1 = mine.w, nchunks = (r1 - r0 + kC - 1) / kC;
+    if ((int64_t)slot0 + nchunks > a.slots) {  // more chunks than these rows have: requests that overlap
         if (tid == 0) report_opt(a.err, DEV_BAD_LENGTHS, b, h, r1);
-        pdl_wait();  // no CTA ends before the chunk kernel has
         return;
     }
     if (warp == 0) tmem_alloc(tslot, 512);
@@ -478,7 +495,6 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const GdnPreA
     tc_fence_after();
     const uint32_t tmem = *tslot, base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const uint32_t smem0 = smem_u32(sm);
-    const int nchunks = (r1 - r0 + kC - 1) / kC;
     const int64_t v_row = (int64_t)H * P;
 
     // Wait for a barrier's phase, a warp at a time; false, for every role, once any wait has run out.
@@ -587,7 +603,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const GdnPreA
             arrive(kBarPutU);
         }
         // All products are done, so that K's and Q's place is free.
-        if (ok && nchunks > 0) ok = wait_for(kBarS, (nchunks - 1) & 1) && wait_for(kBarZq, (nchunks - 1) & 1);
+        if (ok) ok = wait_for(kBarS, (nchunks - 1) & 1) && wait_for(kBarZq, (nchunks - 1) & 1);
         if (ok) {
             float s[32];
             tmem_ld32(s_tm, s);
@@ -666,22 +682,16 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const GdnPreA
                 src += step;
             }
         };
-        int64_t slot0 = 0;
-        if (warp == kFirstIn) {
-            pdl_wait();  // the chunk kernel's operands are there
-            slot0 = a.first[b];
-            if (slot0 + nchunks > a.slots) *sfail = kNoSlots;
-        }
+        if (warp == kFirstIn) pdl_wait();  // the chunk kernel's operands are there
         int copies = 0;
         for (int c = 0; c < nchunks; ++c) {
-            if (warp == kFirstIn && warp_failed(sfail)) break;
             if (c >= 2 && !wait_for(kBarZq, c & 1)) break;  // chunk c - 2's products are done
             load(c);
             if (c >= 2 && !wait_for(kBarO, c & 1)) break;   // and its decays read
             if (warp == kFirstIn && lane == 0) {
                 uint64_t *br = bar + kBarOp + (c & 1);
                 mbar_arrive_expect_tx(br, kSlot);
-                bulk_g2s(sm + L::kOp + (c & 1) * L::kOpStep, a.ws + ((slot0 + c) * H + h) * kSlot, kSlot, br);
+                bulk_g2s(sm + L::kOp + (c & 1) * L::kOpStep, a.ws + ((int64_t)(slot0 + c) * H + h) * kSlot, kSlot, br);
             }
             copies = c + 1;
             cp_async_wait_all();
@@ -752,46 +762,45 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const GdnPreA
     }
     tc_fence_before();
     __syncthreads();
-    if (*sfail && tid == 0) report_opt(a.err, *sfail == kNoSlots ? DEV_BAD_LENGTHS : DEV_PIPE_TIMEOUT, b, h, 0);
+    if (*sfail && tid == 0) report_opt(a.err, DEV_PIPE_TIMEOUT, b, h, 0);
     if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
-// Chunks of requests that do not overlap: at most one more than their share of the rows each.
-int64_t slots_of(int B, int tokens) { return (int64_t)tokens / kC + B; }
-size_t plan_bytes(int B) { return ((size_t)B * sizeof(int32_t) + 255) / 256 * 256; }
+constexpr int kChunkCtas = 4 * 148;  // as many as are resident
 
-cudaError_t launch_after(const void *kernel, dim3 grid, int threads, size_t smem, GdnPreArgs a, cudaStream_t st) {
-    cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    void *args[] = {&a};
-    return cudaLaunchKernelExC(&cfg, kernel, args);
+constexpr int kPlanThreads = 256;
+__global__ void __launch_bounds__(kPlanThreads) gdn_plan_kernel(const GdnPreArgs a) {
+    pdl_trigger();
+    gdn_plan<kPlanThreads>(a);
 }
+
+// Chunks of requests that do not overlap: at most one more than their share of the rows for each that is not short.
+int most_long(int B, int tokens) { return min(B, tokens / (kGdnShort + 1)); }
+int64_t slots_of(int B, int tokens) { return (int64_t)tokens / kC + most_long(B, tokens); }
+size_t plan_bytes(int B) { return ((kPlanOrder + 5 * (size_t)B) * sizeof(int32_t) + 255) / 256 * 256; }
 
 }  // namespace
 
 size_t gdn_chunk_bytes(int B, int H, int tokens) { return plan_bytes(B) + (size_t)(slots_of(B, tokens) * H) * kSlot; }
 
+// Which requests are long is known on the device only, so that every kernel is launched and what it has no work for ends at
+// once.  255 single tokens and one prompt of 2048: 326 us, of 254 and 125 apart (1249 by the recurrence alone); 64 single
+// tokens in arrays of 1000 rows 92 (182 in chunks).  The price is paid where all are short: 64 x 1 token 76 us against 68 by
+// the recurrence alone, 64 x 12 195 against 168, most of it the scan's CTAs, 1.1 us of an SM each to start and end.
 cudaError_t gdn_chunk_launch(GdnPreArgs a, uint8_t *workspace, cudaStream_t st) {
     const int s1 = ChunkSmem::kBytes + 1024, s2 = ScanSmem::kBytes + 1024;
     cudaError_t e = cudaFuncSetAttribute(gdn_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, s1);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(gdn_scan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, s2);
     if (e != cudaSuccess) return e;
     a.slots = (int)slots_of(a.B, a.tokens);
-    a.first = reinterpret_cast<int32_t *>(workspace);
+    a.plan = reinterpret_cast<int32_t *>(workspace);
     a.ws = workspace + plan_bytes(a.B);
+    const int64_t units = (int64_t)a.slots * a.H;
     gdn_plan_kernel<<<1, kPlanThreads, 0, st>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    e = launch_after((const void *)gdn_chunk_kernel, dim3(a.slots, a.H), kChunkThreads, s1, a, st);
-    if (e != cudaSuccess) return e;
-    return launch_after((const void *)gdn_scan_kernel, dim3(a.H * ((a.P + 127) / 128), a.B), kScanThreads, s2, a, st);
+    e = launch_early(gdn_chunk_kernel, dim3((unsigned)min(units, (int64_t)kChunkCtas)), kChunkThreads, s1, a, st);
+    if (e == cudaSuccess) e = launch_early(gdn_scan_kernel, dim3(a.H * ((a.P + 127) / 128), most_long(a.B, a.tokens)), kScanThreads, s2, a, st);
+    return e == cudaSuccess ? gdn_recurrent_launch<__nv_bfloat16>(a, kDk, st) : e;
 }
 
 }  // namespace rssm

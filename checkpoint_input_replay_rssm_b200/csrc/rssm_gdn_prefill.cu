@@ -16,9 +16,8 @@
 //
 // 16 prompts of 1 to 200 tokens, 16 heads, P = N = 64, fp32: 66 us of 6 at the rate of a copy.  The longest prompt
 // decides: about a third of a us a token, most of it the chain products -> shuffles -> state.
-#include "rssm_gdn_prefill.h"
+#include "rssm_gdn_plan.cuh"
 #include "rssm_internal.h"
-#include "rssm_packed.cuh"
 #include "rssm_pair.cuh"
 
 namespace rssm {
@@ -47,13 +46,20 @@ __global__ void __launch_bounds__(32 * kRecWarps) gdn_recurrent_kernel(const Gdn
     __shared__ float sv[2][kRecTok][kRecRows], sa[2][kRecTok], sb[2][kRecTok], skq[kRecTok];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int l8 = lane & 7, g4 = lane >> 3;
+    // Beside the chunked form (plan is set) this kernel has the short requests.
+    const bool beside = N == 128 && sizeof(IN) == 2 && a.plan;
+    // It does not end before the kernels that it was started beside: its first CTA waits for them.
+    auto end = [&] {
+        if (beside && (blockIdx.x | blockIdx.y | blockIdx.z) == 0) pdl_wait();
+    };
     const int h = blockIdx.y, b = blockIdx.z, p0 = blockIdx.x * kRecRows;
     const int rows = min(kRecRows, a.P - p0);
     int r0, r1;
     if (!packed_rows(a.cu, b, a.tokens, r0, r1)) {
         if (tid == 0) report_opt(a.err, DEV_BAD_LENGTHS, b, h, r1);
-        return;
+        return end();
     }
+    if (beside && r1 - r0 > kGdnShort) return end();
     const int64_t head = (int64_t)b * a.H + h;
     const int row0 = 8 * warp + 2 * g4;  // this lane group's rows: row0, row0 + 1 (P is a multiple of 8)
     const bool on = row0 < rows;
@@ -194,16 +200,24 @@ __global__ void __launch_bounds__(32 * kRecWarps) gdn_recurrent_kernel(const Gdn
                 const int at = V == 4 ? (u >> 1) * 32 + l8 * 4 + 2 * (u & 1) : u * 16 + l8 * 2;
                 *reinterpret_cast<u64 *>(a.S_out + (head * a.P + p0 + row0 + r) * N + at) = s[r][u];
             }
+    end();
 }
 
+}  // namespace
+
 template <typename IN>
-cudaError_t launch_recurrent(const GdnPreArgs &a, int N, cudaStream_t st) {
+cudaError_t gdn_recurrent_launch(const GdnPreArgs &a, int N, cudaStream_t st) {
     auto k = N == 16 ? gdn_recurrent_kernel<IN, 16>
                      : N == 32 ? gdn_recurrent_kernel<IN, 32>
                                : N == 64 ? gdn_recurrent_kernel<IN, 64> : gdn_recurrent_kernel<IN, 128>;
-    k<<<dim3((a.P + kRecRows - 1) / kRecRows, a.H, a.B), 32 * kRecWarps, 0, st>>>(a);
+    const dim3 grid((a.P + kRecRows - 1) / kRecRows, a.H, a.B);
+    if (a.plan) return launch_early(k, grid, 32 * kRecWarps, 0, a, st);
+    k<<<grid, 32 * kRecWarps, 0, st>>>(a);
     return cudaGetLastError();
 }
+template cudaError_t gdn_recurrent_launch<__nv_bfloat16>(const GdnPreArgs &, int, cudaStream_t);
+
+namespace {
 
 bool gdn_prefill_valid(const rssm_gdn_prefill_config *c) {
     return c && c->batch >= 1 && c->batch <= 65535 && c->nheads >= 1 && c->nheads <= 65535 && c->headdim >= 8 &&
@@ -212,11 +226,9 @@ bool gdn_prefill_valid(const rssm_gdn_prefill_config *c) {
            (c->input_dtype == RSSM_F32 || c->input_dtype == RSSM_BF16) && c->tokens >= 1;
 }
 
-// The chunked form takes what its tiles are made for, and prompts of more than 12 tokens on average: shorter
-// ones are the state's way in and out, which the recurrence's smaller CTAs overlap better (64 prompts, 32 heads:
-// 1 token 65 us against 179, 8 tokens 132 against 184, 16 tokens 189 against 186, 32 tokens 366 against 193).
+// Whether the call may have requests for the chunked form: what its tiles are made for, and rows for a longer one.
 bool gdn_chunked(const rssm_gdn_prefill_config &c) {
-    return c.dstate == 128 && c.input_dtype == RSSM_BF16 && c.tokens > 12ll * c.batch;
+    return c.dstate == 128 && c.input_dtype == RSSM_BF16 && c.tokens > kGdnShort;
 }
 
 }  // namespace
@@ -246,8 +258,8 @@ RSSM_API rssm_status rssm_gdn_prefill(const rssm_gdn_prefill_config *cfg, const 
     const GdnPreArgs a{c.batch, c.nheads, c.headdim, c.tokens, in->q, in->k, in->v, in->alpha, in->beta,
                        cu, S0, y, S_out, 0, nullptr, nullptr, dev_error};
     const cudaError_t e = gdn_chunked(c) ? gdn_chunk_launch(a, (uint8_t *)workspace, (cudaStream_t)stream)
-                          : c.input_dtype == RSSM_BF16 ? launch_recurrent<__nv_bfloat16>(a, c.dstate, (cudaStream_t)stream)
-                                                     : launch_recurrent<float>(a, c.dstate, (cudaStream_t)stream);
+                          : c.input_dtype == RSSM_BF16 ? gdn_recurrent_launch<__nv_bfloat16>(a, c.dstate, (cudaStream_t)stream)
+                                                       : gdn_recurrent_launch<float>(a, c.dstate, (cudaStream_t)stream);
     return e == cudaSuccess ? RSSM_OK : RSSM_ECUDA;
 }
 

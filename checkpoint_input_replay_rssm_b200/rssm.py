@@ -344,7 +344,8 @@ def gdn_prefill(q, k, v, alpha, beta, cu_seqlens, S0=None, y=None, S_out=None, w
     q, k [tokens, H, N], v [tokens, H, P] bf16 or fp32; alpha, beta [tokens, H] fp32; cu_seqlens
     [B + 1] int32 row offsets of the prompts; S0 [B, H, P, N] fp32 or None (zero).  Returns
     (y [tokens, H, P] fp32, S_out [B, H, P, N] fp32); S_out goes to ``Layer.import_state`` of a GDN
-    layer.  ``err`` (int32 [4], zeroed by the caller) receives device-side inconsistencies.
+    layer.  ``err`` (int32 [4], zeroed by the caller) receives device-side inconsistencies.  Results are within
+    6e-6 (2-norm) for bf16 prompts of more than 12 tokens with N = 128, which are served in chunks, and 1e-7 otherwise.
     """
     import torch
 

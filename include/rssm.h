@@ -275,7 +275,10 @@ RSSM_API rssm_status rssm_mamba2_prefill(const rssm_prefill_config *cfg, const f
  * the state S0 and write every token's output and the fp32 state after the prompt, to be
  * installed with rssm_import_state (the prompt step of a Gated DeltaNet layer, as
  * rssm_mamba2_prefill is of a Mamba-2 layer; the pages on checkpointed input replay describe
- * no prefill).  A request of no tokens copies its S0.
+ * no prefill).  A request of no tokens copies its S0.  A request of more than 12 tokens with
+ * dstate 128 and bf16 inputs is served in chunks of 64 on the tensor cores, with fp32 operands
+ * split into two bf16 parts (6e-6 of the result in the 2-norm), every other one by the recurrence
+ * in fp32 (1e-7); what else is in the batch does not matter to it.
  *   cfg:   batch (1..65535), nheads (1..65535), headdim P and dstate N as for rssm_config,
  *          input_dtype F32 | BF16, tokens = rows of the token arrays (>= 1).
  *   S0:    device fp32 [B][H][P][N], or NULL for a zero state.

@@ -107,3 +107,50 @@ def test_gdn_more_requests_than_one_round_of_the_search():
     want, Sw = _gdn_ref(d, cu, S0)
     _close(y, want, "y")
     _close(S, Sw, "state")
+
+
+@pytest.mark.parametrize("lens", [[1] * 40 + [300] + [2] * 9 + [12, 13, 0], [500] + [1] * 3, [64, 12, 13, 128]])
+def test_gdn_a_request_is_served_the_same_whatever_it_is_packed_with(lens):
+    """Bit for bit, in arrays with and without rows behind the requests: which form serves a request goes by its length."""
+    import torch
+
+    H, P = 2, 128
+    d, cu, S0 = _gdn_inputs(lens, H, 128, P, "bfloat16", 35, pad=100)
+    y, S = _gdn_run(d, cu, S0)
+    want, Sw = _gdn_ref(d, cu, S0)
+    _close(y, want, "y")
+    _close(S, Sw, "state")
+    cut = {n: t[:cu[-1]].contiguous() for n, t in d.items()}
+    y2, S2 = _gdn_run(cut, cu, S0)
+    assert np.array_equal(y2, y[:cu[-1]]) and np.array_equal(S2, S)
+    for b in sorted({lens.index(n) for n in lens if n}):
+        alone = {n: t[cu[b]:cu[b + 1]].contiguous() for n, t in d.items()}
+        y1, S1 = _gdn_run(alone, [0, lens[b]], S0[b:b + 1].contiguous())
+        assert np.array_equal(y1, y[cu[b]:cu[b + 1]]) and np.array_equal(S1[0], S[b]), lens[b]
+    short = [b for b in range(len(lens)) if 0 < lens[b] <= 12]
+    rows = np.concatenate([np.arange(cu[b], cu[b + 1]) for b in short]) if short else np.zeros(0, int)
+    if len(rows):  # fp32 throughout: 2^-24 of the sums' terms, a few dozen of them
+        assert np.abs(y[rows] - want[rows]).max() <= 1e-6 * np.abs(want[rows]).max()
+    assert torch.is_tensor(S0)
+
+
+def test_gdn_long_prompts_beside_single_tokens_are_not_served_token_by_token():
+    """A prompt of 2048 tokens with 255 single tokens takes about as long as the two apart: token by token it would be
+    three times as long."""
+    import torch
+
+    def run(lens):
+        d, cu, S0 = _gdn_inputs(lens, 4, 128, 128, "bfloat16", 36)
+        cud, y, S = _i(cu), torch.empty_like(d["v"], dtype=torch.float32), torch.empty_like(S0)
+        e = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+        best = float("inf")
+        for _ in range(6):
+            e[0].record()
+            rssm.gdn_prefill(d["q"], d["k"], d["v"], d["alpha"], d["beta"], cud, S0, y=y, S_out=S)
+            e[1].record()
+            e[1].synchronize()
+            best = min(best, e[0].elapsed_time(e[1]))
+        return best
+
+    apart = run([2048]) + run([1] * 255)
+    assert run([1] * 255 + [2048]) < 1.6 * apart
