@@ -23,6 +23,13 @@
 // bits and kept as two fp32, so that a difference between neighbours is exact to fp32 however far
 // down the chunk they are.
 //
+// Values that are not finite.  A product over a chunk's tokens meets every token with every other, the later ones with a
+// factor of zero, and zero times an infinity or a NaN is NaN: a token that brings one would reach outputs before it.
+// So the factors are kept finite.  The chunk kernel puts zeros in A and T and hands on the first token that is lost (by k, alpha,
+// beta, or a system that grows past fp32); the scan puts zeros in R from that token on, and from the first such value of v
+// on in its state row.  Outputs of the row from there on and its last state are then NaN, whatever was computed for
+// them.  An infinity or a NaN in q has only its own row of M and column of Y; in S, all that follows in its row is lost.
+//
 // Request b's chunk c has slot first[b] + c, first[] a prefix sum that a kernel before makes (rssm_gdn_plan.cuh).
 // It takes nothing from the offsets on trust; slots at r0 / 64 + b + c, which need no sum, are distinct only where
 // every request's offsets are in order.
@@ -45,7 +52,7 @@ namespace {
 constexpr int kC = kGdnChunk;           // 64 tokens
 constexpr int kDk = 128;                // state columns (N)
 constexpr int kTile = 128 * kC * 2;     // [128 x 64] bf16
-constexpr int kSlot = 2 * kTile + 512;  // hi, lo, then 2^Lam_i and 2^{Lam_C - Lam_i} fp32
+constexpr int kSlot = 2 * kTile + 528;  // hi, lo, then 2^Lam_i and 2^{Lam_C - Lam_i} fp32, then the first lost token
 
 // Eight fp32 values as 16-byte chunks of their (hi, lo) parts.  The conversions are the two-value ones: the
 // one-value form runs at an eighth of their rate.
@@ -62,6 +69,21 @@ __device__ __forceinline__ void split8(const float *v, uint4 &hi, uint4 &lo) {
         ph[e] = h;
         pl[e] = bf16x2(v[2 * e] - __uint_as_float(h << 16), v[2 * e + 1] - __uint_as_float(h & 0xffff0000u));
     }
+}
+// Whether all n values are finite: one multiply-add a value.
+template <int n> __device__ __forceinline__ bool all_finite(const float *v) {
+    float z[2] = {0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < n; ++j) z[j & 1] = fmaf(v[j], 0.f, z[j & 1]);
+    return z[0] + z[1] == 0.f;
+}
+// n values of row i of a factor as a product may have them, *first the first row that was not finite.
+template <int n> __device__ __forceinline__ void keep_finite(float *v, int i, int *first) {
+    if (all_finite<n>(v)) return;
+    atomicMin(first, i);
+#pragma unroll
+    for (int j = 0; j < n; ++j)
+        if (!isfinite(v[j])) v[j] = 0.f;
 }
 __device__ __forceinline__ void bulk_s2g(void *dst, const void *src, uint32_t bytes) {
     asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
@@ -101,10 +123,12 @@ __device__ __forceinline__ bool chunk_unit(const GdnPreArgs &a, uint8_t *sm, uin
         if (lane == 0) {
             sfound[0] = lo;
             sfound[1] = slot - first[lo];
+            sfound[2] = kC;
         }
     }
     __syncthreads();
     const int b = sfound[0], c = sfound[1];
+    int *slost = sfound + 2;
     int r0, r1;
     const bool work = c < gdn_chunks(a, b, r0, r1);
     const int t0 = work ? r0 + c * kC : 0;
@@ -159,6 +183,7 @@ __device__ __forceinline__ bool chunk_unit(const GdnPreArgs &a, uint8_t *sm, uin
                 lamh[t] = (float)s;
                 laml[t] = (float)(s - (double)(float)s);
                 sbeta[t] = be[e];
+                if (!(s < 128.0)) atomicMin(slost, t);  // not a number, or past fp32
                 sg[t] = exp2f((float)(ref - s));
                 out[t] = exp2f((float)s);  // decays that the scan wants
                 out[kC + t] = exp2f((float)(end - s));
@@ -198,6 +223,12 @@ __device__ __forceinline__ bool chunk_unit(const GdnPreArgs &a, uint8_t *sm, uin
                 if (blk <= last_blk) {  // warp-uniform
                     tmem_ld16(base + j0, gv);
                     if ((i >> 4) == blk) {
+                        if (is_k) {  // |k_i|^2 shows what k_i holds
+                            float kk = 0.f;
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) kk = j0 + j == i ? gv[j] : kk;
+                            if (!isfinite(kk)) atomicMin(slost, i);
+                        }
 #pragma unroll
                         for (int j = 0; j < 16; j += 4) {
                             const float4 h4 = *reinterpret_cast<const float4 *>(lamh + j0 + j);
@@ -223,6 +254,7 @@ __device__ __forceinline__ bool chunk_unit(const GdnPreArgs &a, uint8_t *sm, uin
                     for (int j = 0; j < 16; ++j) gv[j] = 0.f;
                 }
                 if (is_k) {
+                    keep_finite<16>(gv, i, slost);
 #pragma unroll
                     for (int j = 0; j < 16; j += 4)
                         *reinterpret_cast<float4 *>(sA + i * kLd + j0 + j) = make_float4(gv[j], gv[j + 1], gv[j + 2], gv[j + 3]);
@@ -280,8 +312,12 @@ __device__ __forceinline__ bool chunk_unit(const GdnPreArgs &a, uint8_t *sm, uin
                             s.y = fmaf((&x.x)[e], y.y, s.y);
                         }
                     }
-                    if (pass) *reinterpret_cast<float2 *>(sA + (d0 + 16 + r) * kLd + d0 + c0) = make_float2(-s.x, -s.y);
-                    else *reinterpret_cast<float2 *>(sA + (d0 + r) * kLd + d0 + 16 + c0) = s;
+                    if (pass) {
+                        *reinterpret_cast<float2 *>(sA + (d0 + 16 + r) * kLd + d0 + c0) = make_float2(-s.x, -s.y);
+                    } else {
+                        keep_finite<2>(&s.x, d0 + 16 + r, slost);
+                        *reinterpret_cast<float2 *>(sA + (d0 + r) * kLd + d0 + 16 + c0) = s;
+                    }
                     __syncthreads();
                 }
             }
@@ -305,8 +341,12 @@ __device__ __forceinline__ bool chunk_unit(const GdnPreArgs &a, uint8_t *sm, uin
                             s.x = fmaf(xe, y.x, s.x); s.y = fmaf(xe, y.y, s.y); s.z = fmaf(xe, y.z, s.z); s.w = fmaf(xe, y.w, s.w);
                         }
                     }
-                    if (pass) *reinterpret_cast<float4 *>(sA + (32 + lane) * kLd + c0) = make_float4(-s.x, -s.y, -s.z, -s.w);
-                    else *reinterpret_cast<float4 *>(sA + lane * kLd + 32 + c0) = s;
+                    if (pass) {
+                        *reinterpret_cast<float4 *>(sA + (32 + lane) * kLd + c0) = make_float4(-s.x, -s.y, -s.z, -s.w);
+                    } else {
+                        keep_finite<4>(&s.x, 32 + lane, slost);
+                        *reinterpret_cast<float4 *>(sA + lane * kLd + 32 + c0) = s;
+                    }
                     __syncthreads();
                 }
             }
@@ -323,6 +363,7 @@ __device__ __forceinline__ bool chunk_unit(const GdnPreArgs &a, uint8_t *sm, uin
 #pragma unroll
                         for (int e = 0; e < 4; ++e) v[j + e] = q0 + 8 * k + j + e <= ti ? (&t4.x)[e] * (&b4.x)[e] : 0.f;
                     }
+                    keep_finite<8>(v, ti, slost);
                     uint4 hi, lo;
                     split8(v, hi, lo);
                     *reinterpret_cast<uint4 *>(sHi + sw128_chunk(ti, (q0 >> 3) + k, 128)) = hi;
@@ -367,6 +408,7 @@ __device__ __forceinline__ bool chunk_unit(const GdnPreArgs &a, uint8_t *sm, uin
                 fence_async_smem();
                 __syncthreads();
                 if (tid == 0) {
+                    *reinterpret_cast<int *>(a.ws + ((int64_t)slot * H + h) * kSlot + 2 * kTile + 512) = *slost;
                     bulk_s2g(a.ws + ((int64_t)slot * H + h) * kSlot, sHi, 2 * kTile);
                     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                     asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
@@ -440,7 +482,8 @@ struct ScanSmem {
     static constexpr int kV = kOp + 2 * kOpStep;      // v [64 tokens][128 p] bf16, two buffers
     static constexpr int kO = kV + 2 * kC * 256;      // o [64 tokens][128 p] fp32
     static constexpr int kBar = kO + kC * 512;
-    static constexpr int kBytes = kBar + 144;
+    static constexpr int kLost = kBar + 144;  // first token of each state row that is lost to a value that is not finite
+    static constexpr int kBytes = kLost + 512;
 };
 constexpr int kChainWarps = 16, kOutWarps = 4, kInWarps = 3;
 constexpr int kFirstIn = kChainWarps + kOutWarps, kIssuer = kFirstIn + kInWarps;
@@ -490,6 +533,8 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const GdnPreA
         *sfail = 0;
         mbar_init_fence();
     }
+    volatile int *slost = reinterpret_cast<volatile int *>(sm + L::kLost);
+    if (tid < 128) slost[tid] = 0x7fffffff;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -574,18 +619,29 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const GdnPreA
             }
             // R^T = V^T - Y^T 2^Lam (behind the prompt v and K are zero, and so is this).
             if (!(ok = wait_for(kBarIn + par, (c >> 1) & 1))) break;
-            float x[16];
-            uint16_t v[16];
+            float x[16], v[16];
             const uint16_t *vs = reinterpret_cast<const uint16_t *>(sm + L::kV + par * kC * 256) + 16 * grp * 128 + row;
 #pragma unroll
-            for (int j = 0; j < 16; ++j) v[j] = vs[j * 128];
+            for (int j = 0; j < 16; ++j) v[j] = bf16_bits_to_float(vs[j * 128]);
+            const int lost = reinterpret_cast<const int *>(dec)[2 * kC];  // first lost token of the chunk
+            const bool losing = __any_sync(0xffffffffu, !all_finite<16>(v) || lost < kC);
             if (!(ok = wait_for(kBarYk, par))) break;
             tmem_ld16(base + kTmY + 16 * grp, x);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const float4 e = reinterpret_cast<const float4 *>(dec + 16 * grp)[k];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) x[4 * k + j] = fmaf(-(&e.x)[j], x[4 * k + j], bf16_bits_to_float(v[4 * k + j]));
+                for (int j = 0; j < 4; ++j) x[4 * k + j] = fmaf(-(&e.x)[j], x[4 * k + j], v[4 * k + j]);
+            }
+            if (losing) {
+                int at = lost < kC ? lost : kC;
+#pragma unroll
+                for (int j = 15; j >= 0; --j)
+                    if (!isfinite(v[j])) at = min(at, 16 * grp + j);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) x[j] = 16 * grp + j >= at ? 0.f : x[j];
+                if (at < kC) atomicMin(const_cast<int *>(slost) + row, kC * c + at);
+                __syncwarp();
             }
             put16(x, kTmR + 8 * grp, kTmR + 32 + 8 * grp);
             tmem_st_wait();
@@ -607,6 +663,9 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const GdnPreA
         if (ok) {
             float s[32];
             tmem_ld32(s_tm, s);
+            if (slost[row] != 0x7fffffff)
+#pragma unroll
+                for (int j = 0; j < 32; ++j) s[j] = NAN;
             st = reinterpret_cast<float *>(sm + L::kKQ);  // [128 p][128 n]
 #pragma unroll
             for (int j = 0; j < 8; ++j)
@@ -649,6 +708,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const GdnPreA
                 }
             }
             arrive(kBarO);
+            for (int t = max(0, slost[ot] - kC * c); t < kC; ++t) so[t * 128 + ot] = NAN;
             if (!meet()) break;
             const int t0 = r0 + c * kC, at = lane * 4;
             float *dst = a.y + (int64_t)t0 * v_row + (int64_t)h * P + p_base + at;

@@ -278,12 +278,15 @@ RSSM_API rssm_status rssm_mamba2_prefill(const rssm_prefill_config *cfg, const f
  * no prefill).  A request of no tokens copies its S0.  A request of more than 12 tokens with
  * dstate 128 and bf16 inputs is served in chunks of 64 on the tensor cores, with fp32 operands
  * split into two bf16 parts (6e-6 of the result in the 2-norm), every other one by the recurrence
- * in fp32 (1e-7); what else is in the batch does not matter to it.
+ * in fp32 (1e-7); what else is in the batch does not matter to it.  An infinity or a NaN among the
+ * inputs reaches the outputs of its token and of later ones of its request and head, and the state
+ * (in v: those of its channel; in q: of its token only), never an earlier output.
  *   cfg:   batch (1..65535), nheads (1..65535), headdim P and dstate N as for rssm_config,
  *          input_dtype F32 | BF16, tokens = rows of the token arrays (>= 1).
  *   S0:    device fp32 [B][H][P][N], or NULL for a zero state.
- *   in:    q, k [tokens][H][N], v [tokens][H][P] in input_dtype, alpha (>= 0), beta
- *          [tokens][H] fp32; the other fields are ignored.
+ *   in:    q, k [tokens][H][N], v [tokens][H][P] in input_dtype, alpha (>= 0; where it is above 1
+ *          its product over 64 tokens is below 2^128), beta [tokens][H] fp32; the other fields are
+ *          ignored.
  *   cu:    device int32[B+1] as above, cu[B] <= tokens.
  *   y:     device fp32 [tokens][H][P]; rows of no request are left as they were.
  *   S_out: device fp32 [B][H][P][N] (may not alias S0).

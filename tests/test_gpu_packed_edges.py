@@ -154,3 +154,61 @@ def test_gdn_long_prompts_beside_single_tokens_are_not_served_token_by_token():
 
     apart = run([2048]) + run([1] * 255)
     assert run([1] * 255 + [2048]) < 1.6 * apart
+
+
+def _same_where_finite(got, want, what):
+    """Not finite at the same places, and the tolerance elsewhere."""
+    lost = ~np.isfinite(want)
+    assert np.array_equal(~np.isfinite(got), lost), (what, np.argwhere(~np.isfinite(got) != lost)[:5])
+    _close(got[~lost], want[~lost], what)
+
+
+@pytest.mark.parametrize("lens", [[150, 20, 40], [9, 20, 40]])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("name", ["q", "k", "v", "alpha", "beta"])
+def test_gdn_what_is_not_finite_reaches_no_earlier_output(name, value, lens):
+    """One value at token 70 (or 5, and at the first one of the next request): outputs before it, of the other heads, of
+    other requests and (in v) of the other channels are what they are without it.  In chunks and by the recurrence."""
+    H, P = 2, 72
+    d, cu, S0 = _gdn_inputs(lens, H, 128, P, "bfloat16", 37)
+    for t, h in ((70 if lens[0] > 70 else 5, 1), (cu[1], 0)):
+        d[name][(t, h) if d[name].dim() == 2 else (t, h, 40)] = value
+    with np.errstate(invalid="ignore"):
+        want, Sw = _gdn_ref(d, cu, S0)
+    y, S = _gdn_run(d, cu, S0)
+    _same_where_finite(y, want, "y")
+    _same_where_finite(S, Sw, "state")
+    assert np.isfinite(y[:5]).all() and np.isfinite(y[cu[2]:]).all() and not np.isfinite(y).all()
+
+
+@pytest.mark.parametrize("first", [0, 15, 16, 17, 31, 47, 63])
+def test_gdn_a_nan_key_anywhere_in_a_chunk(first):
+    """At every place where the triangular system is put together from blocks."""
+    d, cu, S0 = _gdn_inputs([130], 1, 128, 64, "bfloat16", 38)
+    d["k"][64 + first, 0, 3] = float("nan")
+    with np.errstate(invalid="ignore"):
+        want, Sw = _gdn_ref(d, cu, S0)
+    y, S = _gdn_run(d, cu, S0)
+    _same_where_finite(y, want, "y")
+    assert np.isfinite(y[:64 + first]).all() and np.isnan(y[64 + first:]).all() and np.isnan(S).all()
+
+
+def test_gdn_a_state_that_outgrows_fp32_leaves_earlier_outputs():
+    """One key of length 3 throughout, full strength: the state grows eightfold a token, past fp32 at about the 43rd.  The
+    outputs of the tokens before are sums of terms eight times the next smaller one, so that each keeps 4 * 2^-18 of itself
+    times 8 / 7 from the geometric sum of the terms, twice for the two products: below 1e-4; with fp32's last 2 binades left out."""
+    import torch
+
+    d, cu, S0 = _gdn_inputs([64], 1, 128, 64, "bfloat16", 39)
+    k = torch.zeros_like(d["k"])
+    k[:, :, 3] = 3.0
+    d["k"], d["q"], d["alpha"], d["beta"] = k, k.clone(), torch.ones_like(d["alpha"]), torch.ones_like(d["beta"])
+    want, _ = _gdn_ref(d, cu, S0)
+    y, S = _gdn_run(d, cu, S0)
+    size = np.sqrt((want ** 2).mean((1, 2)))
+    fits = np.abs(want).max((1, 2)) < 2.0 ** 120
+    assert 30 < fits.sum() < 50
+    far = np.sqrt(((y - want)[fits] ** 2).mean((1, 2)))
+    assert (far <= 1e-4 * size[fits]).all(), (far / size[fits]).max()
+    assert not np.isfinite(y[-1]).any() and not np.isfinite(S[0, 0, :, 3]).any()
+
