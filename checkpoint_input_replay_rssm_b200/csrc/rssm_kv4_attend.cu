@@ -188,14 +188,13 @@ __global__ void __launch_bounds__(32 * kWarps4, MT == 1 ? 3 : 2) attend_kernel(c
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
         const int ex = row_exponent(top);
-        // 2^-ex as two factors: one alone may leave fp32's range.  The score's factor is
-        // kept above 0 (its sign goes to the query, a zero scale becomes a zero query), so
-        // that the largest raw score is the largest score and a masked one stays -inf.
+        // 2^-ex as two factors: one alone may leave fp32's range.
         const float s0 = copysignf(pow2f(-(ex / 2)), a.scale);
         const float s1 = a.scale == 0.f ? 0.f : pow2f(-(ex - ex / 2));
         if (c == 0) {
-            sf[16 * mt + g + 8 * u] = fmaxf(fabsf(a.scale) * pow2f(ex / 2) * pow2f(ex - ex / 2), 1.2e-38f);
-            sseen[16 * mt + g + 8 * u] = live ? len - n + i + 1 : 0;
+            const int seen = live ? len - n + i + 1 : 0;
+            sf[16 * mt + g + 8 * u] = row_factor(a.scale, ex, top, seen > 0);
+            sseen[16 * mt + g + 8 * u] = seen;
         }
         uint32_t *dst = reinterpret_cast<uint32_t *>(sq) + (mt * KS * 32 + lane) * 4 + u;
 #pragma unroll

@@ -64,6 +64,14 @@ __device__ __forceinline__ int row_exponent(float top) {
 // 2^e for e in -126 .. 127.
 __device__ __forceinline__ float pow2f(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
+// The factor of a row's raw scores: `scale` and the row's power of two, above 0 so that the largest raw score is the largest
+// score and a masked one stays -inf (the sign of `scale` goes to the query, a zero scale becomes a zero query).  A query with an
+// infinity makes every visible score NaN, as inf - inf in the softmax does: left as -inf they would be as if masked.
+__device__ __forceinline__ float row_factor(float scale, int ex, float top, bool sees) {
+    if (top == INFINITY && sees) return NAN;
+    return fmaxf(fabsf(scale) * pow2f(ex / 2) * pow2f(ex - ex / 2), 1.2e-38f);
+}
+
 // The kernel for tiles of 128 rows (rssm_kv4_attend_tiles.cu).
 cudaError_t attend_tiles_launch(const AttendArgs &a, cudaStream_t st);
 

@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
             const int ex = row_exponent(top);
             const float s0 = copysignf(pow2f(-(ex / 2)), a.scale);
             const float s1 = a.scale == 0.f ? 0.f : pow2f(-(ex - ex / 2));
-            f = fmaxf(fabsf(a.scale) * pow2f(ex / 2) * pow2f(ex - ex / 2), 1.2e-38f);
+            f = row_factor(a.scale, ex, top, seen > 0);
             if (st == 0) {
 #pragma unroll
                 for (int k = 0; k < D / 8; ++k) {

@@ -10,7 +10,7 @@ import pytest
 
 from checkpoint_input_replay_rssm_b200 import rssm
 from oracle import packed
-from tests.test_gpu_packed import _close, _cu, _err, _gdn_inputs, _gdn_ref, _gdn_run, _i, _np, _t, _tables_case, _tables_run
+from tests.test_gpu_packed import _attend_case, _attend_check, _attend_run, _close, _err, _gdn_inputs, _gdn_ref, _gdn_run, _i, _np, _t, _tables_case, _tables_run
 
 pytestmark = pytest.mark.gpu
 
@@ -212,3 +212,22 @@ def test_gdn_a_state_that_outgrows_fp32_leaves_earlier_outputs():
     assert (far <= 1e-4 * size[fits]).all(), (far / size[fits]).max()
     assert not np.isfinite(y[-1]).any() and not np.isfinite(S[0, 0, :, 3]).any()
 
+
+
+# ---------------------------------------------------------------- attention over the 4-bit cache
+@pytest.mark.parametrize("lens,news,Hq,Hk", [([5, 30], [8, 1], 4, 2), ([200, 30, 300], [150, 40, 129], 16, 1), ([4000, 30], [1, 40], 8, 2)])
+@pytest.mark.parametrize("sign", [-1, 1])
+def test_attend_an_infinite_query_is_nan_where_it_sees_and_zero_where_it_sees_nothing(lens, news, Hq, Hk, sign):
+    """One visible token, whose score is -inf or +inf: exp(s - max) is that of inf - inf.  The other rows are as without it."""
+    c = _attend_case(51 + Hq, lens, news, Hq, Hk, 128, 16)
+    b = int(np.argmax(np.array(news) > np.array(lens)))  # a request whose first rows see nothing
+    clean = _attend_run(c)
+    one, none = c["cu"][b] + news[b] - lens[b], c["cu"][b] + news[b] - lens[b] - 1
+    key = c["K"][b][0, 1 // (Hq // Hk)]
+    d = int(np.argmax(np.abs(key)))
+    for row in (one, none):
+        c["q"][row, 1, d] = sign * float(np.sign(key[d])) * float("inf")
+    got = _attend_run(c)
+    assert np.isnan(got[one, 1]).all() and not got[none].any()
+    got[one, 1] = clean[one, 1] = 0
+    assert np.array_equal(got, clean)
