@@ -52,7 +52,8 @@ class HybridStack:
 
     ssm_mode: "replay" (checkpoint + read copy ``read_dtype`` + buffer) or "eager"
     (fp32 state rewritten every token).  kv_cache: "bf16" (a dense cache, torch attention)
-    or "fp4" (the paged 4-bit cache and its attention, pages of ``page_size`` tokens).
+    or "fp4" (the paged 4-bit cache and its attention, pages of ``page_size`` tokens; what the device
+    refuses there raises ``rssm.RssmError`` from ``check_cache``, or from a later ``step``).
     Weights, initial states and the cached keys/values come from a seeded torch generator.
     """
 
@@ -126,6 +127,8 @@ class HybridStack:
         self.free_head, self.cached_len = torch.zeros(1, **i32), torch.zeros(s.batch, **i32)
         self.one_new = torch.ones(s.batch, **i32)
         self.kv_err = torch.zeros(4, **i32)
+        self.kv_seen = torch.zeros(4, dtype=torch.int32, pin_memory=True)  # kv_err after some step
+        self.kv_event = torch.cuda.Event()
         slots = None
         if s.context:
             slots = self._tables(torch.full((s.batch,), s.context, **i32), s.batch * s.context)[2]
@@ -136,6 +139,25 @@ class HybridStack:
                 p["cache"] = rssm.kv4_cache(s.batch * width, s.n_kv_heads, ps, s.head_dim, device=self.device)
                 if slots is not None:
                     rssm.kv4_append(k, v, slots, p["cache"], k_scale=self.KV_SCALE, v_scale=self.KV_SCALE, err=self.kv_err)
+        self.check_cache()
+
+    def check_cache(self):
+        """Wait for the steps so far and raise where one of the 4-bit cache's operators was refused on the device."""
+        if self.kv_cache == "fp4":
+            self._raise_if(self.kv_err)
+
+    def _raise_if(self, err):
+        code, b, h, value = err.tolist()
+        if code:
+            raise self.rssm.RssmError(self.rssm.RSSM_EDEVICE, f"4-bit attention cache: device error {code}, request {b}, "
+                                                              f"head {h}, value {value}")
+
+    def _watch(self):
+        """The error word as far as it has come to the host, without waiting: a refused step does not pass for long."""
+        if self.kv_event.query():
+            self._raise_if(self.kv_seen)
+            self.kv_seen.copy_(self.kv_err, non_blocking=True)
+            self.kv_event.record()
 
     def _tables(self, new_len, max_tokens):
         self.tables = self.rssm.build_tables(self.cached_len, new_len, self.free_pages, self.free_head, self.block_table,
@@ -201,6 +223,7 @@ class HybridStack:
         if self.kv_cache == "fp4":
             if self.torch.cuda.is_current_stream_capturing():
                 raise RuntimeError("a step of the stack advances counters on the host, which a replayed graph would not")
+            self._watch()
             self._tables(self.one_new, self.s.batch)
         for kind, p in self.layers:
             x = self._ssm(x, p) if kind == "ssm" else self._attn(x, p)

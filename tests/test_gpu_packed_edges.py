@@ -9,6 +9,7 @@ import numpy as np
 import pytest
 
 from checkpoint_input_replay_rssm_b200 import rssm
+from checkpoint_input_replay_rssm_b200.hybrid import HybridShape, HybridStack
 from oracle import packed
 from tests.test_gpu_packed import _attend_case, _attend_check, _attend_run, _close, _err, _gdn_inputs, _gdn_ref, _gdn_run, _i, _np, _t, _tables_case, _tables_run
 
@@ -231,3 +232,32 @@ def test_attend_an_infinite_query_is_nan_where_it_sees_and_zero_where_it_sees_no
     assert np.isnan(got[one, 1]).all() and not got[none].any()
     got[one, 1] = clean[one, 1] = 0
     assert np.array_equal(got, clean)
+
+
+# ---------------------------------------------------------------- the hybrid stack on the 4-bit cache
+def _stack(**kw):
+    shape = HybridShape(batch=3, blocks=1, ssm_per_block=1, d_model=256, nheads=4, headdim=32, dstate=64, ngroups=2, window=4,
+                        n_q_heads=8, n_kv_heads=2, head_dim=64, context=61)
+    return HybridStack(shape, seed=7, max_steps=20, kv_cache="fp4", page_size=16, **kw)
+
+
+def test_hybrid_stack_says_when_its_cache_refused_a_step():
+    import torch
+
+    st = _stack()
+    x = torch.zeros((3, 256), dtype=torch.bfloat16, device="cuda")
+    for _ in range(3):
+        st.step(x)
+        st.check_cache()
+    st.cached_len = st.cached_len - 1000  # the device refuses lengths below 0
+    st.step(x)
+    with pytest.raises(rssm.RssmError, match="device error 4, request 0") as e:
+        st.check_cache()
+    assert e.value.status == rssm.RSSM_EDEVICE
+    with pytest.raises(rssm.RssmError, match="device error 4"):  # without being asked, by the step after the next at the latest
+        for _ in range(3):
+            torch.cuda.synchronize()
+            st.step(x)
+    full = HybridStack(st.s, seed=7, max_steps=4)
+    full.step(x)
+    full.check_cache()  # nothing to check
