@@ -82,18 +82,22 @@ __global__ void __launch_bounds__(32 * kWarps4, MT == 1 ? 3 : 2) attend_kernel(c
     const int split = blockIdx.x, tile = blockIdx.y % a.tiles, h = blockIdx.y / a.tiles, b = blockIdx.z;
     const int ps = a.kv.ps, G = a.G;
     if (a.splits > 1) pdl_trigger();  // the joining kernel's CTAs may start, up to their wait
+    // Beside the kernel of the 128-row tiles, which it may have been started before the end of, it does not end before that.
+    auto end = [&] {
+        if (a.few && (split | blockIdx.y | b) == 0) pdl_wait();
+    };
     int r0, n, len;
     if (!attend_request(a, b, r0, n, len)) {
         if (tid == 0) report_opt(a.err, DEV_BAD_LENGTHS, b, 0, len);
-        return;
+        return end();
     }
     const int rows = n * G, row0 = tile * RT;
-    if (row0 >= rows) return;
+    if (row0 >= rows || !attend_mine(a, rows, false)) return end();
     // tokens that the tile's last row sees
     const int last = min(row0 + RT, rows) - 1;
     const int tlen = max(0, len - n + last / G + 1);
     const int ns = max(1, (tlen + a.L - 1) / a.L);
-    if (split >= ns) return;
+    if (split >= ns) return end();
     const int t_begin = split * a.L, t_end = min(tlen, t_begin + a.L);
     const int first_seen = len - n + row0 / G + 1;  // tokens that the tile's first row sees
 
@@ -493,6 +497,7 @@ __global__ void __launch_bounds__(32 * kWarps4, MT == 1 ? 3 : 2) attend_kernel(c
             }
         }
     }
+    end();
 }
 
 // Join the splits of a tile's rows: out = sum_s 2^{m_s - m} O_s / sum_s 2^{m_s - m} l_s.  D / 4 threads have a row, or,
@@ -513,7 +518,7 @@ __global__ void __launch_bounds__(Join<D, MT>::kThreads) attend_join_kernel(cons
     int r0, n, len;
     if (!attend_request(a, b, r0, n, len)) return;  // reported by the first kernel
     const int rows = n * a.G, row0 = tile * RT;
-    if (row0 >= rows) return;
+    if (row0 >= rows || !attend_mine(a, rows, false)) return;
     const int last = min(row0 + RT, rows) - 1;
     const int ns = (max(0, len - n + last / a.G + 1) + a.L - 1) / a.L;
     if (ns <= 1) return;
@@ -562,13 +567,25 @@ __global__ void __launch_bounds__(Join<D, MT>::kThreads) attend_join_kernel(cons
 float score_scale(float sm_scale, float k_scale) { return sm_scale * k_scale * 1.4426950408889634f; }
 
 constexpr int64_t kMaxL = 2048, kWaves = 2;
-constexpr int64_t kTileRows = 128, kTileUnits = 32;
+constexpr int64_t kTileRows = 128, kTileUnits = 32, kPackTiles = 2;
 
 // Sizes of the launch.  Row tiles of 32 where a request can have more than 16 rows.
 struct Plan {
     int mt, tiles, splits, L;
+    int few_mt, packed;  // 128-row tiles: the tiles (x 16 rows) of the kernel beside them, and how they are numbered (AttendArgs)
     size_t bytes;
 };
+
+// Cached tokens of one CTA: a share of the work that fills the machine (148 SMs, 3 CTAs each) kWaves times over,
+// between 256 (a shorter one is all start and join) and kMaxL (a longer one makes a long tail).
+void split_context(int64_t seq, int64_t units, Plan *p) {
+    const int64_t want = 148 * 3 * kWaves;
+    int64_t L = (seq * units + want - 1) / want;
+    L = L < 256 ? 256 : L > kMaxL ? kMaxL : L;
+    L = (L + 127) / 128 * 128;
+    p->splits = (int)((seq + L - 1) / L);
+    p->L = (int)L;
+}
 
 bool attend_plan(const rssm_kv4_config *c, const rssm_attend_config *t, Kv4Args *kv, Plan *p) {
     if (!kv4_args(c, kv) || !t) return false;
@@ -587,18 +604,24 @@ bool attend_plan(const rssm_kv4_config *c, const rssm_attend_config *t, Kv4Args 
     int64_t seq = (int64_t)t->max_pages * kv->ps;
     if (t->max_seq < seq) seq = t->max_seq;
     if (seq > 1 << 30) return false;  // positions and their strides are int32
-    // Tokens of one CTA: a share of the work that fills the machine (148 SMs, 3 CTAs each) kWaves times over,
-    // between 256 (a shorter one is all start and join) and kMaxL (a longer one makes a long tail).
-    const int64_t units = (int64_t)t->batch * kv->Hk * tiles, want = 148 * 3 * kWaves;
-    int64_t L = (seq * units + want - 1) / want;
-    L = L < 256 ? 256 : L > kMaxL ? kMaxL : L;
-    if (p->mt == 8) L = seq;
-    L = (L + 127) / 128 * 128;
-    const int64_t splits = (seq + L - 1) / L;
     p->tiles = (int)tiles;
-    p->splits = (int)splits;
-    p->L = (int)L;
-    p->bytes = splits > 1 ? (size_t)(units * splits * 16 * p->mt) * (size_t)(kv->D + 2) * 4 : 0;
+    // Beside the 128-row tiles, which are not split, single tokens and drafts of one small tile keep the kernel that is:
+    // a prompt's chunk in the batch would else leave each of them to one CTA for its whole context (15 tokens over 32768 and a
+    // chunk of 512: 892 us, apart 66 and 47).
+    const int64_t G = t->n_q_heads / kv->Hk;
+    p->few_mt = p->mt != 8 ? 0 : G <= 16 ? 1 : G <= 32 ? 2 : 0;
+    const int64_t units = (int64_t)t->batch * kv->Hk * (p->few_mt ? 1 : tiles), rows_of = p->few_mt ? p->few_mt : p->mt;
+    if (p->mt == 8 && !p->few_mt) {
+        p->splits = 1;
+        p->L = (int)((seq + 127) / 128 * 128);
+    } else {
+        split_context(seq, units, p);
+    }
+    p->bytes = p->splits > 1 ? (size_t)(units * p->splits * 16 * rows_of) * (size_t)(kv->D + 2) * 4 : 0;
+    // A grid row of tiles for each request is mostly CTAs without work where one of them is long: then the tiles that so many
+    // rows can make are numbered through, and a CTA looks its own up.
+    const int64_t most = (int64_t)t->tokens * G / 128 + (t->batch < t->tokens ? t->batch : t->tokens);
+    p->packed = p->few_mt && t->batch * tiles > kPackTiles * most ? (int)most : 0;
     return true;
 }
 
@@ -606,19 +629,24 @@ template <int D, int MT>
 cudaError_t attend_launch(const AttendArgs &a, cudaStream_t st) {
     cudaError_t e = cudaFuncSetAttribute(attend_kernel<D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D, MT>::kBytes);
     if (e != cudaSuccess) return e;
-    attend_kernel<D, MT><<<dim3(a.splits, a.tiles * a.kv.Hk, a.B), 32 * kWarps4, Smem<D, MT>::kBytes, st>>>(a);
-    if ((e = cudaGetLastError()) != cudaSuccess || a.splits == 1) return e;
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(a.splits, a.tiles * a.kv.Hk, a.B);
+    cfg.blockDim = dim3(32 * kWarps4);
+    cfg.dynamicSmemBytes = Smem<D, MT>::kBytes;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = a.few ? 1 : 0;  // beside the 128-row tiles it need not wait for their end
+    e = cudaLaunchKernelEx(&cfg, attend_kernel<D, MT>, a);
+    if (e != cudaSuccess || a.splits == 1) return e;
     // (one request over 4096 / 20000 tokens: 12.5 / 25 us against 18.6 / 50 with one CTA a tile; 256 requests: 116
     // against 119 the other way about)
     const bool few = (int64_t)a.B * a.tiles * a.kv.Hk < 148;
     cfg.gridDim = dim3(a.tiles * a.kv.Hk * (few ? 16 * MT * 2 * Join<D, MT>::kLanes / Join<D, MT>::kThreads : 1), a.B);
     cfg.blockDim = dim3(Join<D, MT>::kThreads);
-    cfg.stream = st;
-    cfg.attrs = attr;
+    cfg.dynamicSmemBytes = 0;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, attend_join_kernel<D, MT>, a);
 }
@@ -655,9 +683,17 @@ RSSM_API rssm_status rssm_kv4_attend(const rssm_kv4_config *cfg, const rssm_atte
     a.err = dev_error;
     const cudaStream_t st = (cudaStream_t)stream;
     const bool wide = a.kv.D == 128;
-    const cudaError_t e = p.mt == 8   ? attend_tiles_launch(a, st)
-                          : p.mt == 2 ? (wide ? attend_launch<128, 2>(a, st) : attend_launch<64, 2>(a, st))
-                                      : (wide ? attend_launch<128, 1>(a, st) : attend_launch<64, 1>(a, st));
+    cudaError_t e = cudaSuccess;
+    int mt = p.mt;
+    if (mt == 8) {
+        a.few = 16 * p.few_mt;
+        a.packed = p.packed;
+        e = attend_tiles_launch(a, st);
+        a.tiles = 1;
+        mt = p.few_mt;
+    }
+    if (e == cudaSuccess && mt == 2) e = wide ? attend_launch<128, 2>(a, st) : attend_launch<64, 2>(a, st);
+    if (e == cudaSuccess && mt == 1) e = wide ? attend_launch<128, 1>(a, st) : attend_launch<64, 1>(a, st);
     return e == cudaSuccess ? RSSM_OK : RSSM_ECUDA;
 }
 

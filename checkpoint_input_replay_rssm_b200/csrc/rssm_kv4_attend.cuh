@@ -11,6 +11,8 @@ struct AttendArgs {
     Kv4Args kv;
     int B, Hq, G, tokens, max_pages, max_q, max_seq;
     int tiles, splits, L;  // row tiles a request, splits, cached tokens a split
+    int few;               // where both kernels run: requests of up to this many rows are the split one's (0: one kernel has all)
+    int packed;            // the 128-row tiles of all requests are numbered through (at most so many), 0: a grid row a request
     float scale;           // sm_scale * k_scale * log2(e)
     const __nv_bfloat16 *q;
     const uint8_t *cache;
@@ -31,6 +33,9 @@ __device__ __forceinline__ bool attend_request(const AttendArgs &a, int b, int &
     len = a.seq_len[b];
     return ok && n <= a.max_q && len >= 0 && len <= a.max_seq && len <= (int64_t)a.max_pages * a.kv.ps;
 }
+
+// Whether this kernel of the two is to serve a request of so many rows.
+__device__ __forceinline__ bool attend_mine(const AttendArgs &a, int rows, bool tiles) { return a.few == 0 || (rows > a.few) == tiles; }
 
 __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
     uint32_t r;

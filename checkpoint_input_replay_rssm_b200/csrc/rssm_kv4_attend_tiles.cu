@@ -54,6 +54,52 @@ template <int D> struct TilesSmem {
     static_assert(128 * (D + 4) * 4 <= 4 * kTileB, "O overlays the K and V tiles");
 };
 
+// Request and tile of number u of the requests that are this kernel's, by all threads of a CTA; false past the last one.
+__device__ bool find_tile(const AttendArgs &a, int u, int &b, int &tile) {
+    __shared__ long long wsum[kTilesThreads / 32];
+    __shared__ int found[2];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (a.B + kTilesThreads - 1) / kTilesThreads, b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
+    auto tiles_of = [&](int i) {
+        int r0, n, len;
+        const bool ok = attend_request(a, i, r0, n, len) && attend_mine(a, n * a.G, true);
+        return ok ? (n * a.G + 127) / 128 : 0;
+    };
+    long long mine = 0;
+    for (int i = b0; i < b1; ++i) mine += tiles_of(i);
+    long long x = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += v;
+    }
+    if (lane == 31) wsum[warp] = x;
+    __syncthreads();
+    x -= mine;
+    long long all = 0;
+    for (int w = 0; w < kTilesThreads / 32; ++w) {
+        if (w < warp) x += wsum[w];
+        all += wsum[w];
+    }
+    // more tiles than the rows have: requests that overlap
+    if (all > a.packed && u == 0 && tid == 0) report_opt(a.err, DEV_BAD_LENGTHS, -1, 0, (int)min(all, 0x7fffffffll));
+    if (u >= all) return false;
+    if (u >= x && u < x + mine)
+        for (int i = b0; i < b1; ++i) {
+            const int n = tiles_of(i);
+            if (u < x + n) {
+                found[0] = i;
+                found[1] = (int)(u - x);
+                break;
+            }
+            x += n;
+        }
+    __syncthreads();
+    b = found[0];
+    tile = found[1];
+    return true;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const AttendArgs a) {
     using L = TilesSmem<D>;
@@ -67,15 +113,18 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
     int *snan = reinterpret_cast<int *>(sm + L::kNan);
     uint32_t *sgone = reinterpret_cast<uint32_t *>(sm + L::kGone);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int tile = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+    const int h = blockIdx.y;
     const int ps = a.kv.ps, G = a.G;
+    int tile = blockIdx.x, b = blockIdx.z;
+    if (a.few) pdl_trigger();  // the split kernel may start, for the requests that are its own
+    if (a.packed && !find_tile(a, blockIdx.x, b, tile)) return;
     int r0, n, len;
     if (!attend_request(a, b, r0, n, len)) {
         if (tid == 0) report_opt(a.err, DEV_BAD_LENGTHS, b, 0, len);
         return;
     }
     const int rows = n * G, row0 = tile * 128;
-    if (row0 >= rows) return;
+    if (row0 >= rows || !attend_mine(a, rows, true)) return;
     const int last = min(row0 + 128, rows) - 1;
     const int t_end = max(0, len - n + last / G + 1);  // tokens that the tile's last row sees
     const int ntiles = (t_end + 127) / 128;
@@ -444,7 +493,7 @@ template <int D> cudaError_t launch(const AttendArgs &a, cudaStream_t st) {
     const int need = TilesSmem<D>::kBytes + 1024, smem = need > 116 * 1024 ? need : 116 * 1024;
     const cudaError_t e = cudaFuncSetAttribute(attend_tiles_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    attend_tiles_kernel<D><<<dim3(a.tiles, a.kv.Hk, a.B), kTilesThreads, smem, st>>>(a);
+    attend_tiles_kernel<D><<<a.packed ? dim3(a.packed, a.kv.Hk) : dim3(a.tiles, a.kv.Hk, a.B), kTilesThreads, smem, st>>>(a);
     return cudaGetLastError();
 }
 

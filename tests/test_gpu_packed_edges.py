@@ -261,3 +261,95 @@ def test_hybrid_stack_says_when_its_cache_refused_a_step():
     full = HybridStack(st.s, seed=7, max_steps=4)
     full.step(x)
     full.check_cache()  # nothing to check
+
+
+# ---------------------------------------------------------------- attention: single tokens and prompt chunks in one batch
+MIXED = [
+    # news, Hq, Hk, D: most requests single tokens (tiles numbered through), or most of them chunks (a grid row each)
+    ([1] * 20 + [70, 9, 0, 2], 16, 1, 128),
+    ([1] * 9 + [0, 150] + [1] * 6, 16, 2, 64),
+    ([70, 1, 64, 80, 66, 1, 77, 0, 3], 16, 1, 128),
+    ([1] * 30 + [40, 1, 5], 20, 1, 64),     # 20 rows a token: the split kernel has tiles of 32
+    ([1] * 12 + [33, 1, 20], 40, 1, 128),   # 40 rows a token: none
+]
+
+
+@pytest.mark.parametrize("news,Hq,Hk,D", MIXED)
+def test_attend_single_tokens_beside_chunks(news, Hq, Hk, D):
+    r = np.random.default_rng(len(news) + Hq)
+    lens = [int(n + r.integers(0, 700 if n == 1 else 150)) for n in news]
+    lens[0], lens[1] = 1500, 0 if news[1] == 1 else lens[1]  # a long context of its own; a row that sees nothing
+    c = _attend_case(53 + Hq, lens, news, Hq, Hk, D, 32, first=2, pad=4)
+    _attend_check(c, _attend_run(c))
+
+
+@pytest.mark.parametrize("bad", ["offsets", "length", "overlap"])
+def test_attend_a_bad_request_in_a_mixed_batch_spoils_no_other(bad):
+    import torch
+
+    news = [1] * 20 + [70, 9, 1, 2]
+    c = _attend_case(54, [n + 300 for n in news], news, 16, 1, 128, 32)
+    clean = _attend_run(c)
+    cu, lens = list(c["cu"]), [n + 300 for n in news]
+    if bad == "offsets":
+        cu[7] = 10 ** 6  # requests 6 and 7
+        spoilt = {6, 7}
+    elif bad == "length":
+        lens[20] = -1
+        spoilt = {20}
+    else:  # every second request claims all rows up to its own: more tiles than the rows can make
+        cu = [0, 102] * 12 + [0]
+        spoilt = set(range(24))
+    err, out = _err(), torch.full_like(c["q"], 7.25)
+    rssm.kv4_attend(c["q"], c["cache"], c["table"], _i(lens), _i(cu), 102, out=out, err=err, **c["kw"])
+    assert err[0].item() == rssm.RSSM_DEV_BAD_LENGTHS and (err[1].item() in spoilt or err[1].item() == -1)
+    got = _np(out)
+    for b in set(range(24)) - spoilt:
+        rows = slice(c["cu"][b], c["cu"][b + 1])
+        assert np.abs(got[rows] - clean[rows]).max() <= 2.0 ** -7 * np.abs(c["V"][b]).max(), b
+    if bad != "overlap":
+        for b in spoilt:
+            assert (got[c["cu"][b]:c["cu"][b + 1]] == 7.25).all()
+
+
+def test_attend_a_mixed_step_takes_about_as_long_as_its_parts():
+    """15 tokens over 8192 and a chunk of 256: served by one kernel, each token would be one CTA's for its whole context."""
+    import torch
+
+    def run(lens, news):
+        c = _attend_case(55, lens, news, 16, 1, 128, 64)
+        out, cu = torch.empty_like(c["q"]), _i(c["cu"])
+        e = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+        best = float("inf")
+        for _ in range(6):
+            e[0].record()
+            rssm.kv4_attend(c["q"], c["cache"], c["table"], c["lens"], cu, c["max_q"], out=out, **c["kw"])
+            e[1].record()
+            e[1].synchronize()
+            best = min(best, e[0].elapsed_time(e[1]))
+        return best
+
+    apart = run([8192] * 15, [1] * 15) + run([512], [256])
+    assert run([8192] * 15 + [512], [1] * 15 + [256]) < 1.6 * apart
+
+
+@pytest.mark.parametrize("D,ps,n", [(128, 64, 1500), (64, 16, 1300), (128, 256, 2600)])
+def test_attend_tiles_over_many_tiles_of_tokens(D, ps, n):
+    """10 to 21 tiles of tokens a row tile: every barrier and page word of the 128-row kernel in use several times over; scores that
+    grow along the context, so that the running maximum moves in the last tiles too, and ones that do not; a page that
+    is not there in the 6th."""
+    c = _attend_case(56 + D, [n, n - 200, 40], [9, 64, 8], 16, 4, D, ps)
+    got = _attend_run(c)
+    _attend_check(c, got)
+    rise = dict(c, q=(c["q"].float() * 6).to(c["q"].dtype))
+    _attend_check(rise, _attend_run(rise))
+    table = c["table"].clone()
+    at = 700 // ps
+    table[0, at] = -1
+    err = _err()
+    gone = _np(rssm.kv4_attend(c["q"], c["cache"], table, c["lens"], _i(c["cu"]), c["max_q"], err=err, **c["kw"]))
+    assert err[:2].tolist() == [rssm.RSSM_DEV_BAD_PAGE, 0]
+    assert np.array_equal(gone[c["cu"][1]:], got[c["cu"][1]:])
+    keep = np.r_[0:at * ps, min(n, (at + 1) * ps):n]
+    d = dict(c, K=[c["K"][0][keep]], V=[c["V"][0][keep]], q=c["q"][:9], cu=[0, 9])
+    _attend_check(d, gone[:9])
