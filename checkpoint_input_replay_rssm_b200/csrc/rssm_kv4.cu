@@ -7,7 +7,7 @@
 // (1/4, 3/4, 5/4, 7/4, 5/2, 7/2, 5) 3, so that x and border * s, at most 7 bits, are
 // multiples of one unit of x's last place: a quotient that is not on a border is at least
 // 2^-8 of itself away from it.  The quotients are therefore formed as x * (1 / (s g)), which
-// errs by less than 2^-22, and rounded to 13 significant bits, which puts those that belong
+// errs by less than 2^-22, and rounded to 14 significant bits, which puts those that belong
 // on a border back on it and takes no other across one: the stored codes are those of exact
 // arithmetic, at three instructions an element where a division takes about ten.
 //
@@ -68,8 +68,8 @@ __device__ __forceinline__ float e4m3_value(uint32_t b) {
     return __half2float(__ushort_as_half((unsigned short)(r & 0xffff)));
 }
 
-// v to 13 significant bits, to nearest (an infinity stays one).
-__device__ __forceinline__ float to13bits(float v) {
+// v to 14 significant bits (13 behind the leading one), to nearest (an infinity stays one).
+__device__ __forceinline__ float to14bits(float v) {
     return __uint_as_float((__float_as_uint(v) + 0x200u) & 0xfffffc00u);
 }
 
@@ -123,8 +123,8 @@ __global__ void __launch_bounds__(kKvThreads) kv4_append_kernel(const Kv4Args a,
         uint32_t c[2] = {0, 0};
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            c[j >> 2] |= e2m1x2(to13bits(__uint_as_float(x[j] << 16) * inv_s),
-                                to13bits(__uint_as_float(x[j] & 0xffff0000u) * inv_s))
+            c[j >> 2] |= e2m1x2(to14bits(__uint_as_float(x[j] << 16) * inv_s),
+                                to14bits(__uint_as_float(x[j] & 0xffff0000u) * inv_s))
                          << (8 * (j & 3));
         *reinterpret_cast<uint2 *>(dst + off * (D >> 1) + 8 * blk) = some ? make_uint2(c[0], c[1]) : make_uint2(0, 0);
         dst[a.ps * (D >> 1) + off * nb + blk] = (uint8_t)sb;

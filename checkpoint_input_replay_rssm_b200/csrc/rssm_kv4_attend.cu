@@ -607,7 +607,7 @@ bool attend_plan(const rssm_kv4_config *c, const rssm_attend_config *t, Kv4Args 
     p->tiles = (int)tiles;
     // Beside the 128-row tiles, which are not split, single tokens and drafts of one small tile keep the kernel that is:
     // a prompt's chunk in the batch would else leave each of them to one CTA for its whole context (15 tokens over 32768 and a
-    // chunk of 512: 892 us, apart 66 and 47).
+    // chunk of 512 over 2048: 892 us, now 102, apart 66 and 47).
     const int64_t G = t->n_q_heads / kv->Hk;
     p->few_mt = p->mt != 8 ? 0 : G <= 16 ? 1 : G <= 32 ? 2 : 0;
     const int64_t units = (int64_t)t->batch * kv->Hk * (p->few_mt ? 1 : tiles), rows_of = p->few_mt ? p->few_mt : p->mt;
@@ -619,7 +619,9 @@ bool attend_plan(const rssm_kv4_config *c, const rssm_attend_config *t, Kv4Args 
     }
     p->bytes = p->splits > 1 ? (size_t)(units * p->splits * 16 * rows_of) * (size_t)(kv->D + 2) * 4 : 0;
     // A grid row of tiles for each request is mostly CTAs without work where one of them is long: then the tiles that so many
-    // rows can make are numbered through, and a CTA looks its own up.
+    // rows can make are numbered through, and a CTA looks its own up.  (The grid's CTAs over the tiles: 1.7, 8 chunks of 100 to
+    // 512, 272 us against 311 numbered through; 2.1, one of 512 and 7 of 200, 161 against 162; 5, one of 512 and 31 of 100, 211
+    // against 201; 46, one of 512 and 255 tokens, 127 numbered through.)
     const int64_t most = (int64_t)t->tokens * G / 128 + (t->batch < t->tokens ? t->batch : t->tokens);
     p->packed = p->few_mt && t->batch * tiles > kPackTiles * most ? (int)most : 0;
     return true;

@@ -13,7 +13,7 @@
 // Roles: 8 softmax warps (4 a stream, the first of which issues the stream's products) and 8 widening warps (16 tokens
 // each, the next tile's bytes in registers ahead).  They meet on barriers in shared memory; every wait is bounded.
 //
-// 8 prompts' chunks of 100 to 512 tokens behind up to 4096, 16 query heads a key/value head of 128: 181 us of 41 at
+// 8 prompts' chunks of 100 to 512 tokens behind up to 4096, 16 query heads a key/value head of 128: 184 us of 41 at
 // the rate of a library product.  A tile takes about 1.7 us, not the 0.55 that its products ask for: a stream's score
 // read, maximum, exponentials and stores are one chain of which two streams hide a half, and a CTA's start (queries,
 // first pages) is 10 us.

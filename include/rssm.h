@@ -265,7 +265,8 @@ RSSM_API rssm_status rssm_mamba2_prefill(const rssm_prefill_config *cfg, const f
  * descending).  They hold no handle: each takes its sizes in a config, enqueues on `stream`
  * (a cudaStream_t on the current device, NULL = legacy default stream), allocates nothing and
  * does not synchronise, so each can be captured in a graph.  Two calls in flight may share
- * inputs but not outputs or workspace.  `dev_error` (device int32[4] or NULL) receives
+ * inputs but not outputs or workspace; within a call no output overlaps an input or another output.
+ * `dev_error` (device int32[4] or NULL) receives
  * {code, request, head, value} of the first inconsistency that only the device can see and is
  * otherwise left alone; the caller zeroes it.  Host-visible misuse is RSSM_EINVAL with nothing
  * enqueued. */
@@ -354,7 +355,8 @@ RSSM_API size_t rssm_kv4_cache_bytes(const rssm_kv4_config *cfg);
 
 /* Write `tokens` >= 1 rows of k and v (device bf16 [tokens][n_kv_heads][head_dim]) to the slots
  * slot_map[t].  A negative slot is skipped; one past the cache sets RSSM_DEV_BAD_PAGE.  Slots
- * of one call are distinct (of two rows with one slot, either or a mixture of blocks stays). */
+ * of one call are distinct (of two rows with one slot neither may stay: what the slot then holds is
+ * unspecified). */
 RSSM_API rssm_status rssm_kv4_append(const rssm_kv4_config *cfg, int32_t tokens, const void *k, const void *v,
                                      const int32_t *slot_map, void *cache, int32_t *dev_error, void *stream);
 /* The values held at the given slots as bf16 [tokens][n_kv_heads][head_dim] each; a row whose

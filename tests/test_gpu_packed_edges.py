@@ -353,3 +353,53 @@ def test_attend_tiles_over_many_tiles_of_tokens(D, ps, n):
     keep = np.r_[0:at * ps, min(n, (at + 1) * ps):n]
     d = dict(c, K=[c["K"][0][keep]], V=[c["V"][0][keep]], q=c["q"][:9], cu=[0, 9])
     _attend_check(d, gone[:9])
+
+
+# ---------------------------------------------------------------- writing the 4-bit cache
+@pytest.mark.parametrize("T,Hk,D,ps", [(37, 2, 128, 16), (129, 8, 128, 256), (300, 3, 64, 48)])
+def test_append_leaves_every_byte_of_other_slots(T, Hk, D, ps):
+    """A cache full of some bytes: behind a write of some slots, and one that skips half of them, every byte that belongs to
+    another slot is as it was; the others are those of a write into a cache of zeros."""
+    import torch
+
+    r = np.random.default_rng(T)
+    pages = -(-T // ps) + 1
+    slots = r.permutation(pages * ps)[:T]
+    k, v = (_t(r.normal(size=(T, Hk, D)), "bfloat16") for _ in range(2))
+
+    def of_slots(some):
+        """Bool [pages, Hk, bytes]: the bytes that belong to these slots."""
+        m = np.zeros((pages, 2, ps, D // 2 + D // 16), bool)  # keys and values: codes and scales of a token
+        m[np.asarray(some) // ps, :, np.asarray(some) % ps] = True
+        codes, scales = m[..., :D // 2].reshape(pages, 2, -1), m[..., D // 2:].reshape(pages, 2, -1)
+        page = np.concatenate([codes[:, 0], scales[:, 0], codes[:, 1], scales[:, 1]], 1)
+        return np.broadcast_to(page[:, None], (pages, Hk, page.shape[1]))
+
+    for used in (np.arange(T), np.arange(T)[::2]):
+        named = np.full(T, -1)
+        named[used] = slots[used]
+        cache, zeros = (torch.full((pages, Hk, ps * D * 9 // 8), fill, dtype=torch.uint8, device="cuda") for fill in (0xA5, 0))
+        for c in (cache, zeros):
+            rssm.kv4_append(k, v, _i(named), c, k_scale=0.25, v_scale=0.5)
+        got, mine = cache.cpu().numpy(), of_slots(slots[used])
+        assert (got[~mine] == 0xA5).all()
+        assert np.array_equal(got[mine], zeros.cpu().numpy()[mine])
+
+
+def test_operators_repeat_themselves_bit_for_bit():
+    """The same call twice, and once more beside other work: no result hangs on the order in which CTAs end."""
+    import torch
+
+    c = _attend_case(57, [3000, 700, 40, 900], [1, 3, 1, 40], 16, 1, 128, 64)
+    d, cu, S0 = _gdn_inputs([1, 300, 12, 70, 0, 5], 4, 128, 128, "bfloat16", 58)
+    first = None
+    for n in range(3):
+        if n == 2:
+            noise = torch.randn(2048, 2048, device="cuda")
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(20):
+                    noise = noise @ noise * 1e-2
+        got = [_attend_run(c), *_gdn_run(d, cu, S0)]
+        first = first or got
+        for a, b in zip(got, first):
+            assert np.array_equal(a, b)
