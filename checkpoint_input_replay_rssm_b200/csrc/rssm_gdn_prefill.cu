@@ -219,16 +219,18 @@ template cudaError_t gdn_recurrent_launch<__nv_bfloat16>(const GdnPreArgs &, int
 
 namespace {
 
+int gdn_dtype(const rssm_gdn_prefill_config &c) { return c.input_dtype & ~RSSM_GDN_FP32; }
+
 bool gdn_prefill_valid(const rssm_gdn_prefill_config *c) {
     return c && c->batch >= 1 && c->batch <= 65535 && c->nheads >= 1 && c->nheads <= 65535 && c->headdim >= 8 &&
            c->headdim <= 256 && c->headdim % 8 == 0 &&
            (c->dstate == 16 || c->dstate == 32 || c->dstate == 64 || c->dstate == 128) &&
-           (c->input_dtype == RSSM_F32 || c->input_dtype == RSSM_BF16) && c->tokens >= 1;
+           (gdn_dtype(*c) == RSSM_F32 || gdn_dtype(*c) == RSSM_BF16) && c->tokens >= 1;
 }
 
 // Whether the call may have requests for the chunked form: what its tiles are made for, and rows for a longer one.
 bool gdn_chunked(const rssm_gdn_prefill_config &c) {
-    return c.dstate == 128 && c.input_dtype == RSSM_BF16 && c.tokens > kGdnShort;
+    return c.dstate == 128 && c.input_dtype == RSSM_BF16 && c.tokens > kGdnShort;  // (and not by the recurrence on request)
 }
 
 }  // namespace
@@ -258,8 +260,8 @@ RSSM_API rssm_status rssm_gdn_prefill(const rssm_gdn_prefill_config *cfg, const 
     const GdnPreArgs a{c.batch, c.nheads, c.headdim, c.tokens, in->q, in->k, in->v, in->alpha, in->beta,
                        cu, S0, y, S_out, 0, nullptr, nullptr, dev_error};
     const cudaError_t e = gdn_chunked(c) ? gdn_chunk_launch(a, (uint8_t *)workspace, (cudaStream_t)stream)
-                          : c.input_dtype == RSSM_BF16 ? gdn_recurrent_launch<__nv_bfloat16>(a, c.dstate, (cudaStream_t)stream)
-                                                       : gdn_recurrent_launch<float>(a, c.dstate, (cudaStream_t)stream);
+                          : gdn_dtype(c) == RSSM_BF16 ? gdn_recurrent_launch<__nv_bfloat16>(a, c.dstate, (cudaStream_t)stream)
+                                                      : gdn_recurrent_launch<float>(a, c.dstate, (cudaStream_t)stream);
     return e == cudaSuccess ? RSSM_OK : RSSM_ECUDA;
 }
 

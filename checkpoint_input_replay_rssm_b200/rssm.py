@@ -19,6 +19,7 @@ RSSM_OK, RSSM_EINVAL, RSSM_ESTATE, RSSM_ECUDA, RSSM_EDEVICE = range(5)
 RSSM_MAMBA2, RSSM_GDN, RSSM_KDA = 0, 1, 2
 RSSM_REPLAY, RSSM_EAGER = 0, 1
 RSSM_F32, RSSM_BF16, RSSM_FP8E4M3 = 0, 1, 2
+RSSM_GDN_FP32 = 256
 RSSM_DEV_BAD_ACCEPT, RSSM_DEV_BAD_COUNTERS, RSSM_DEV_PIPE_TIMEOUT = 1, 2, 3
 RSSM_DEV_BAD_LENGTHS, RSSM_DEV_NO_PAGES, RSSM_DEV_BAD_PAGE = 4, 5, 6
 DTYPES = {"f32": RSSM_F32, "bf16": RSSM_BF16, "fp8": RSSM_FP8E4M3}
@@ -338,14 +339,15 @@ def _ok(st, what):
 
 
 def gdn_prefill(q, k, v, alpha, beta, cu_seqlens, S0=None, y=None, S_out=None, workspace=None, err=None,
-                stream=None):
+                stream=None, fp32=False):
     """Torch convenience over rssm_gdn_prefill: the gated delta rule over packed prompts.
 
     q, k [tokens, H, N], v [tokens, H, P] bf16 or fp32; alpha, beta [tokens, H] fp32; cu_seqlens
     [B + 1] int32 row offsets of the prompts; S0 [B, H, P, N] fp32 or None (zero).  Returns
     (y [tokens, H, P] fp32, S_out [B, H, P, N] fp32); S_out goes to ``Layer.import_state`` of a GDN
     layer.  ``err`` (int32 [4], zeroed by the caller) receives device-side inconsistencies.  Results are within
-    6e-6 (2-norm) for bf16 prompts of more than 12 tokens with N = 128, which are served in chunks, and 1e-7 otherwise.
+    6e-6 (2-norm) for bf16 prompts of more than 12 tokens with N = 128, which are served in chunks, and 1e-7 otherwise;
+    ``fp32=True`` has all of them served by the fp32 recurrence, at a third of a microsecond a token.
     """
     import torch
 
@@ -362,7 +364,8 @@ def gdn_prefill(q, k, v, alpha, beta, cu_seqlens, S0=None, y=None, S_out=None, w
         y = q.new_empty((T, H, P), dtype=f32) if y is None else y
         S_out = q.new_empty((Bn, H, P, N), dtype=f32) if S_out is None else S_out
         lib = load()
-        cfg = ctypes.byref(rssm_gdn_prefill_config(Bn, H, P, N, RSSM_BF16 if dt is torch.bfloat16 else RSSM_F32, T))
+        kind = (RSSM_BF16 if dt is torch.bfloat16 else RSSM_F32) + (RSSM_GDN_FP32 if fp32 else 0)
+        cfg = ctypes.byref(rssm_gdn_prefill_config(Bn, H, P, N, kind, T))
         _, ws, nb = _workspace(workspace, lib.rssm_gdn_prefill_workspace_bytes(cfg), dev, q)
         ins = rssm_inputs(q=_want("q", q, dt, (T, H, N), dev), k=_want("k", k, dt, (T, H, N), dev),
                           v=_want("v", v, dt, (T, H, P), dev), alpha=_want("alpha", alpha, f32, (T, H), dev),

@@ -279,11 +279,12 @@ RSSM_API rssm_status rssm_mamba2_prefill(const rssm_prefill_config *cfg, const f
  * no prefill).  A request of no tokens copies its S0.  A request of more than 12 tokens with
  * dstate 128 and bf16 inputs is served in chunks of 64 on the tensor cores, with fp32 operands
  * split into two bf16 parts (6e-6 of the result in the 2-norm), every other one by the recurrence
- * in fp32 (1e-7); what else is in the batch does not matter to it.  An infinity or a NaN among the
+ * in fp32 (1e-7); what else is in the batch does not matter to it.  RSSM_GDN_FP32 in input_dtype
+ * chooses the recurrence for all (a third of a microsecond a token).  An infinity or a NaN among the
  * inputs reaches the outputs of its token and of later ones of its request and head, and the state
  * (in v: those of its channel; in q: of its token only), never an earlier output.
  *   cfg:   batch (1..65535), nheads (1..65535), headdim P and dstate N as for rssm_config,
- *          input_dtype F32 | BF16, tokens = rows of the token arrays (>= 1).
+ *          input_dtype F32 | BF16 (+ RSSM_GDN_FP32), tokens = rows of the token arrays (>= 1).
  *   S0:    device fp32 [B][H][P][N], or NULL for a zero state.
  *   in:    q, k [tokens][H][N], v [tokens][H][P] in input_dtype, alpha (>= 0; where it is above 1
  *          its product over 64 tokens is below 2^128), beta [tokens][H] fp32; the other fields are
@@ -298,9 +299,10 @@ RSSM_API rssm_status rssm_mamba2_prefill(const rssm_prefill_config *cfg, const f
  * it were alone, but for those that share rows with one another: they hold unspecified values, or
  * are skipped with the same code where together they claim more rows than there are.
  * {RSSM_DEV_PIPE_TIMEOUT, b, h, token} is set if a tensor-core wait gives up (2 s). */
+#define RSSM_GDN_FP32 256
 typedef struct {
     int32_t batch, nheads, headdim, dstate;
-    int32_t input_dtype; /* F32 | BF16 */
+    int32_t input_dtype; /* F32 | BF16, + RSSM_GDN_FP32 */
     int32_t tokens;      /* rows of q, k, v, alpha, beta and y */
 } rssm_gdn_prefill_config;
 RSSM_API size_t rssm_gdn_prefill_workspace_bytes(const rssm_gdn_prefill_config *cfg);

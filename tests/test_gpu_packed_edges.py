@@ -157,6 +157,18 @@ def test_gdn_long_prompts_beside_single_tokens_are_not_served_token_by_token():
     assert run([1] * 255 + [2048]) < 1.6 * apart
 
 
+@pytest.mark.parametrize("lens", [[300, 1, 0, 65], [700]])
+def test_gdn_in_fp32_on_request(lens):
+    """bf16 prompts that are served in chunks otherwise.  The recurrence rounds each of a token's sums to 2^-24 of itself; over
+    700 tokens whose decays and writes forget, a few dozen such roundings are alive: 1e-6 of the result in the 2-norm is room
+    for all of them at their worst, and a sixth of what chunks leave."""
+    d, cu, S0 = _gdn_inputs(lens, 2, 128, 128, "bfloat16", 41)
+    want, Sw = _gdn_ref(d, cu, S0)
+    y, S = _gdn_run(d, cu, S0, fp32=True)
+    for got, w in ((y, want), (S, Sw)):
+        assert np.sqrt(((got - w) ** 2).sum()) <= 1e-6 * np.sqrt((w ** 2).sum())
+
+
 def _same_where_finite(got, want, what):
     """Not finite at the same places, and the tolerance elsewhere."""
     lost = ~np.isfinite(want)

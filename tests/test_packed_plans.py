@@ -20,8 +20,15 @@ def test_gdn_workspace_goes_by_what_the_rows_can_hold():
     # one prompt and many single tokens may be in any batch of so many rows
     assert _gdn_bytes(256, 2303) >= 36 * 4 * 2 * 128 * 64 * 2
     assert _gdn_bytes(1, 10 ** 5) > _gdn_bytes(1, 10 ** 4) and _gdn_bytes(100, 10 ** 4) >= _gdn_bytes(1, 10 ** 4)
-    for kw in (dict(dstate=64), dict(input_dtype=rssm.RSSM_F32)):
+    for kw in (dict(dstate=64), dict(input_dtype=rssm.RSSM_F32), dict(input_dtype=rssm.RSSM_BF16 + rssm.RSSM_GDN_FP32)):
         assert _gdn_bytes(4, 1000, **kw) == 0
+
+
+@pytest.mark.parametrize("kind", [rssm.RSSM_FP8E4M3 + rssm.RSSM_GDN_FP32, 512, -1, 3])
+def test_gdn_input_types_refused(kind):
+    cfg = rssm.rssm_gdn_prefill_config(1, 4, 128, 128, kind, 10)
+    ins = rssm.rssm_inputs(**{n: P16 for n in ("q", "k", "v", "alpha", "beta")})
+    assert rssm.load().rssm_gdn_prefill(ctypes.byref(cfg), None, ctypes.byref(ins), P16, P16, P16, P16, 1 << 40, None, None) == rssm.RSSM_EINVAL
 
 
 def _attend_bytes(batch, Hq, tokens, max_pages, max_q, max_seq, Hk=2):
