@@ -34,12 +34,12 @@
 // It takes nothing from the offsets on trust; slots at r0 / 64 + b + c, which need no sum, are distinct only where
 // every request's offsets are in order.
 //
-// 64 prompts of 1 to 1024 tokens (34500 in all), 32 heads, P = 128: 394 us for the chunk kernel and 472 for the
-// scan, of 259 at the rate of a copy for both (together 2.0 TB/s of what a call has to move).  The chunk kernel is
-// bound by the issue of its fp32 work in shared memory (2.0 instructions a cycle at four CTAs an SM, which its
-// shared memory and registers allow).  The scan is a chain: 2.6 us a chunk of a prompt, three products that wait
+// 64 prompts of 1 to 1024 tokens (34500 in all), 32 heads, P = 128: 412 us for the chunk kernel and 500 for the
+// scan, of 259 at the rate of a copy for both (together 1.9 TB/s of what a call has to move).  The chunk kernel is
+// bound by its short fp32 steps out of shared memory: warps wait at the barriers between them, and that pipe is 67% busy (four
+// CTAs an SM, which its shared memory and registers allow).  The scan is a chain: 2.7 us a chunk of a prompt, three products that wait
 // for each other and the conversions between them, with one CTA an SM, and about 13 us to start and end a CTA.  One
-// prompt of 8191 tokens: 94 and 330 us.
+// prompt of 8191 tokens: 98 and 355 us.
 #include <cuda_bf16.h>
 
 #include "rssm_gdn_plan.cuh"

@@ -28,10 +28,9 @@
 //
 // 256 requests of 4096 tokens, 2 heads of 128, 16 rows a tile: 116 us, 54% of the rate of a copy while it
 // streams and 40% with the CTAs' start, tail and join; one request over 4096 tokens: 12.5 us,
-// 8.5 of them start, one range and its end.  What bounds it in between is the issue of instructions, of which a
-// matrix instruction takes 8 slots and the widening of its operands about as many: a 16-row tile uses half of
-// the columns that a 16 x 8 product offers, so that more rows a tile are nearly free (32 rows: two products for one
-// widening).  Widening to shared memory first, wider copies and fewer warps with more stages were slower; a third
+// 8.5 of them start, one range and its end.  What bounds it in between is latency at 12 warps an SM: conversions, products and
+// exponentials that wait for the one before use 53% of the issue slots and a third of the tensor pipe.  More rows a tile are
+// nearly free (32 rows: two products for one widening).  Widening to shared memory first, wider copies and fewer warps with more stages were slower; a third
 // CTA on the SM (160 registers a thread) is worth more than any of them.
 #include <math.h>
 
