@@ -415,3 +415,57 @@ def test_operators_repeat_themselves_bit_for_bit():
         first = first or got
         for a, b in zip(got, first):
             assert np.array_equal(a, b)
+
+
+# ---------------------------------------------------------------- calls that follow one another closely, and at once
+def test_calls_back_to_back_in_one_workspace_and_at_once_on_three_streams():
+    """The delta rule and the attention launch kernels that start before the one in front has ended.  Call after call in the
+    same workspace and outputs, on one stream and on three at once (each with its own), every result is bit for bit that
+    of the call alone."""
+    import torch
+
+    sets = []
+    for seed in (71, 72, 73):
+        r = np.random.default_rng(seed)
+        lens = [int(n) for n in np.where(r.random(20) < 0.6, r.integers(0, 13, 20), r.integers(13, 260, 20))]
+        d, cu, S0 = _gdn_inputs(lens, 4, 128, 128, "bfloat16", seed, pad=int(r.integers(0, 200)))
+        news = [1] * 18 + [40, 70, 0, 3]
+        c = _attend_case(seed, [n + int(r.integers(0, 600)) for n in news], news, 16, 1, 128, 32)
+        sets.append((d, _i(cu), S0, c, _i(c["cu"])))
+
+    def run(s, y, S, out, ws):
+        d, cu, S0, c, cuq = s
+        rssm.gdn_prefill(d["q"], d["k"], d["v"], d["alpha"], d["beta"], cu, S0, y=y, S_out=S, workspace=ws)
+        rssm.kv4_attend(c["q"], c["cache"], c["table"], c["lens"], cuq, c["max_q"], out=out, workspace=ws, **c["kw"])
+
+    def outputs(s):
+        return [torch.zeros((s[0]["q"].shape[0], 4, 128), device="cuda"), torch.zeros_like(s[2]), torch.zeros_like(s[3]["q"]),
+                torch.full((1 << 26,), 0xFF, dtype=torch.uint8, device="cuda")]
+
+    want = []
+    for s in sets:
+        o = outputs(s)
+        run(s, *o)
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in o[:3]])
+    # one stream, one workspace, the sets in turn
+    outs = [outputs(s) for s in sets]
+    for o in outs[1:]:
+        o[3] = outs[0][3]
+    for _ in range(30):
+        for s, o in zip(sets, outs):
+            run(s, *o)
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert all(torch.equal(a, b) for a, b in zip(o[:3], w))
+    # three streams at once
+    outs = [outputs(s) for s in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    for n in range(30):
+        for s, o, st in zip(sets, outs, streams):
+            with torch.cuda.stream(st):
+                run(s, *o)
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert all(torch.equal(a, b) for a, b in zip(o[:3], w))
